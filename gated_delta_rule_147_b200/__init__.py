@@ -7,6 +7,10 @@ Entry points (CUDA, sm_100a, through the C ABI in include/gdr.h):
   gdr_chunk_fwd / chunk_fwd     whole-sequence forward, chunkwise on tcgen05
   gdr_chunk_bwd / chunk_bwd     its backward pass (gradients of every input)
   gdr_decode_step / decode_step one token per head, state updated in place
+and the operators around the recurrence (layers.py):
+  conv_fwd / conv_bwd / conv_step     short causal depthwise convolution
+  qk_norm_fwd / qk_norm_bwd           per-head norm of q and k, with the rotation
+  scan_fwd / scan_bwd / scan_step     selective state-space scan
 
 torch is used for device memory and streams only; every step of the
 recurrence runs in the library's kernels. Importing this package does not
@@ -19,6 +23,19 @@ from ._lib import (GATE_CHANNEL, GATE_NONE, GATE_SCALAR, GATE_TIED, GDR_BF16, GD
                    gdr_chunk_bwd_grouped, gdr_chunk_bwd_grouped_workspace_size,
                    gdr_chunk_bwd_workspace_size, gdr_chunk_fwd, gdr_chunk_fwd_grouped, gdr_chunk_fwd_static, gdr_chunk_fwd_workspace_size,
                    gdr_decode_step, gdr_decode_step_grouped, load)
+
+_LAYERS = ("conv_fwd", "conv_bwd", "conv_step", "scan_fwd", "scan_bwd", "scan_step", "qk_norm_fwd",
+           "qk_norm_bwd")
+
+
+def __getattr__(name):
+    # layers.py imports torch, which this package leaves to the first call
+    if name in _LAYERS:
+        from . import layers
+        globals().update({n: getattr(layers, n) for n in _LAYERS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 TIED = "tied"
 _KIND = {"none": GATE_NONE, "scalar": GATE_SCALAR, "channel": GATE_CHANNEL, "tied": GATE_TIED}

@@ -16,12 +16,18 @@ GDR_OK, GDR_ERR_INVALID_ARG, GDR_ERR_UNSUPPORTED, GDR_ERR_MISALIGNED, GDR_ERR_LA
 GDR_DEVICE_TIMEOUT, GDR_DEVICE_DECAY_RANGE = 1, 2
 GDR_BF16, GDR_FP32 = 0, 1
 GATE_NONE, GATE_SCALAR, GATE_CHANNEL, GATE_TIED = 0, 1, 2, 3
+ACT_NONE, ACT_SILU = 0, 1
+NORM_L2, NORM_RMS = 0, 1
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
 
 EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_grouped", "gdr_chunk_fwd_workspace_size",
            "gdr_chunk_fwd_static", "gdr_chunk_fwd_static_capacity", "gdr_chunk_bwd",
            "gdr_chunk_bwd_workspace_size", "gdr_chunk_bwd_grouped",
            "gdr_chunk_bwd_grouped_workspace_size", "gdr_decode_step",
-           "gdr_decode_step_grouped", "gdr_selftest_bounded_wait", "gdr_status_string",
+           "gdr_decode_step_grouped", "gdr_conv_fwd", "gdr_conv_bwd",
+           "gdr_conv_bwd_workspace_size", "gdr_conv_step", "gdr_scan_fwd", "gdr_scan_bwd",
+           "gdr_scan_bwd_workspace_size", "gdr_scan_step", "gdr_qk_norm_fwd", "gdr_qk_norm_bwd",
+           "gdr_qk_norm_bwd_workspace_size", "gdr_selftest_bounded_wait", "gdr_status_string",
            "gdr_version")
 
 _lock = threading.Lock()
@@ -73,6 +79,21 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.gdr_chunk_bwd_grouped_workspace_size.restype = sz
         lib.gdr_decode_step.argtypes = [vp] * 6 + [ip] * 3 + [vp, vp] + [ip] * 5 + [vp, vp]
         lib.gdr_decode_step.restype = ip
+        fp = ctypes.c_float
+        for fn, args in (("gdr_conv_fwd", [vp] * 8 + [ip] * 7 + [vp]),
+                         ("gdr_conv_bwd", [vp] * 12 + [sz, vp] + [ip] * 8 + [vp]),
+                         ("gdr_conv_step", [vp] * 6 + [ip] * 6 + [vp]),
+                         ("gdr_scan_fwd", [vp] * 13 + [ip] * 7 + [vp]),
+                         ("gdr_scan_bwd", [vp] * 22 + [sz, vp] + [ip] * 8 + [vp]),
+                         ("gdr_scan_step", [vp] * 11 + [ip] * 6 + [vp]),
+                         ("gdr_qk_norm_fwd", [vp] * 9 + [ip] * 8 + [fp] * 3 + [ip] * 3 + [vp]),
+                         ("gdr_qk_norm_bwd", [vp] * 13 + [sz, vp] + [ip] * 8 + [fp] * 3 + [ip] * 4 + [vp])):
+            getattr(lib, fn).argtypes = args
+            getattr(lib, fn).restype = ip
+        for fn, n in (("gdr_conv_bwd_workspace_size", 4), ("gdr_scan_bwd_workspace_size", 5),
+                      ("gdr_qk_norm_bwd_workspace_size", 1)):
+            getattr(lib, fn).argtypes = [ip] * n
+            getattr(lib, fn).restype = sz
         lib.gdr_status_string.argtypes = [ip]
         lib.gdr_status_string.restype = ctypes.c_char_p
         lib.gdr_version.restype = ip
@@ -190,6 +211,43 @@ def gdr_decode_step(q, k, v, alpha, b, w, alpha_kind, b_kind, w_kind, S, o, B, H
                                 _stream(stream))
     if st != GDR_OK:
         raise GdrError("gdr_decode_step", st)
+
+
+def _layer_call(name, argc):
+    """A layer entry point: the C arguments in their order, tensors by device
+    pointer, then the stream. `argc` counts them without the stream."""
+    def call(*args, stream=None) -> None:
+        if len(args) != argc:
+            raise TypeError(f"{name} takes {argc} arguments and the stream, got {len(args)}")
+        st = getattr(_handle or load(), name)(*[a.data_ptr() if hasattr(a, "data_ptr") else a for a in args],
+                                              _stream(stream))
+        if st != GDR_OK:
+            raise GdrError(name, st)
+    call.__name__ = call.__qualname__ = name
+    call.__doc__ = f"Same arguments as the C entry point {name} (include/gdr.h)."
+    return call
+
+
+gdr_conv_fwd = _layer_call("gdr_conv_fwd", 15)
+gdr_conv_bwd = _layer_call("gdr_conv_bwd", 22)
+gdr_conv_step = _layer_call("gdr_conv_step", 12)
+gdr_scan_fwd = _layer_call("gdr_scan_fwd", 20)
+gdr_scan_bwd = _layer_call("gdr_scan_bwd", 32)
+gdr_scan_step = _layer_call("gdr_scan_step", 17)
+gdr_qk_norm_fwd = _layer_call("gdr_qk_norm_fwd", 23)
+gdr_qk_norm_bwd = _layer_call("gdr_qk_norm_bwd", 30)
+
+
+def gdr_conv_bwd_workspace_size(B, T, D, W) -> int:
+    return int(load().gdr_conv_bwd_workspace_size(B, T, D, W))
+
+
+def gdr_scan_bwd_workspace_size(B, T, D, N, G) -> int:
+    return int(load().gdr_scan_bwd_workspace_size(B, T, D, N, G))
+
+
+def gdr_qk_norm_bwd_workspace_size(d) -> int:
+    return int(load().gdr_qk_norm_bwd_workspace_size(d))
 
 
 def gdr_selftest_bounded_wait(d_status, stream=None) -> None:

@@ -19,8 +19,8 @@ OBJDIR = os.path.join(ROOT, "_build")
 SOURCES = ["api.cu", "decode.cu", "recurrent.cu", "chunk_sm100.cu", "chunk_erasefree_sm100.cu",
            "chunk_bwd.cu", "chunk_bwd_tc_sm100.cu", "chunk_bwd_grad_sm100.cu",
            "chunk_twopass_sm100.cu", "chunk_twopass256_sm100.cu", "chunk_twopass_general_sm100.cu", "selftest.cu",
-           "static_scratch.cu"]
-HEADERS = ["common.cuh", "chunk_common.cuh", "rcp_seed.h"]
+           "static_scratch.cu", "conv.cu", "scan.cu", "scan_bwd.cu", "scan_api.cu", "qk_norm.cu"]
+HEADERS = ["common.cuh", "chunk_common.cuh", "rcp_seed.h", "layer_common.cuh", "scan_common.cuh"]
 LIB = os.path.join(HERE, "libgdr.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMPILE_FLAGS = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -1,0 +1,124 @@
+// Shared device helpers of the layer operators (short convolution, selective
+// scan, query/key norm): vector loads and stores with conversion, the
+// activations, packed fp32 pairs, and the launch as a programmatic dependent.
+#pragma once
+
+#include "common.cuh"
+
+namespace gdr {
+
+// V consecutive elements as floats; one or two 16-byte (or one 8-byte) loads
+// when V > 1, which needs the address aligned to the access.
+template <typename T, int V> struct VecIO;
+template <typename T> struct VecIO<T, 1> {
+    static __device__ __forceinline__ void load(float* f, const T* p) { f[0] = to_f32(*p); }
+    static __device__ __forceinline__ void store(T* p, const float* f) { *p = from_f32<T>(f[0]); }
+};
+template <> struct VecIO<float, 4> {
+    static __device__ __forceinline__ void load(float* f, const float* p) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    }
+    static __device__ __forceinline__ void store(float* p, const float* f) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+};
+template <> struct VecIO<float, 8> {
+    static __device__ __forceinline__ void load(float* f, const float* p) {
+        VecIO<float, 4>::load(f, p);
+        VecIO<float, 4>::load(f + 4, p + 4);
+    }
+    static __device__ __forceinline__ void store(float* p, const float* f) {
+        VecIO<float, 4>::store(p, f);
+        VecIO<float, 4>::store(p + 4, f + 4);
+    }
+};
+__device__ __forceinline__ void unpack_bf16x2(uint32_t u, float& lo, float& hi) {
+    lo = __uint_as_float(u << 16);
+    hi = __uint_as_float(u & 0xffff0000u);
+}
+template <> struct VecIO<__nv_bfloat16, 4> {
+    static __device__ __forceinline__ void load(float* f, const __nv_bfloat16* p) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        unpack_bf16x2(u.x, f[0], f[1]);
+        unpack_bf16x2(u.y, f[2], f[3]);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+    }
+};
+template <> struct VecIO<__nv_bfloat16, 8> {
+    static __device__ __forceinline__ void load(float* f, const __nv_bfloat16* p) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        unpack_bf16x2(u.x, f[0], f[1]);
+        unpack_bf16x2(u.y, f[2], f[3]);
+        unpack_bf16x2(u.z, f[4], f[5]);
+        unpack_bf16x2(u.w, f[6], f[7]);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                  pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    }
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + e^-x) from the hardware exponential and reciprocal; e^-x = inf
+// gives 0. Relative error a few 2^-23 (the exponent's argument is rounded once).
+__device__ __forceinline__ float sigmoidf_fast(float x) {
+    return __fdividef(1.f, 1.f + ex2_approx(-x * kLog2e));
+}
+
+// log(1 + e^x) = max(x, 0) + log1p(e^-|x|). With y = e^-|x| in (0, 1] and
+// s = y / (2 + y) in (0, 1/3], log1p(y) = 2 atanh(s) = 2 s sum_k s^2k / (2k+1):
+// relative accuracy is kept for y -> 0 (large negative x), which log(1 + y)
+// loses. Terms up to s^14: the first one dropped, s^16 / 17, is below 2^-29.
+__device__ __forceinline__ float softplusf_series(float x) {
+    const float y = ex2_approx(-fabsf(x) * kLog2e);
+    const float s = __fdividef(y, 2.f + y), s2 = s * s;
+    float r = 1.f / 15.f;
+    r = fmaf(r, s2, 1.f / 13.f);
+    r = fmaf(r, s2, 1.f / 11.f);
+    r = fmaf(r, s2, 1.f / 9.f);
+    r = fmaf(r, s2, 1.f / 7.f);
+    r = fmaf(r, s2, 1.f / 5.f);
+    r = fmaf(r, s2, 1.f / 3.f);
+    r = fmaf(r, s2, 1.f);
+    return fmaxf(x, 0.f) + 2.f * s * r;
+}
+
+// Tokens of sequence b: lengths[b] held to [0, T], or T without lengths.
+__device__ __forceinline__ int seq_len(const int* lengths, int b, int T) {
+    return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
+// A kernel launched with launch_dependent() starts while the previous kernel
+// of the stream drains; nothing may be read before this returns.
+__device__ __forceinline__ void dependent_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void dependent_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem,
+                             cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+// Host checks shared by the entry points.
+inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline size_t dtype_size(int dtype) { return dtype == GDR_BF16 ? 2 : 4; }
+inline bool dtype_ok(int dtype) { return dtype == GDR_BF16 || dtype == GDR_FP32; }
+inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace gdr

@@ -374,6 +374,178 @@ gdr_status gdr_decode_step_grouped(const void* q, const void* k, const void* v,
                                    void* stream);
 
 /*
+ * Layer operators
+ * ---------------
+ * What stands around the recurrence in the layers that use it: the short
+ * causal convolution of q, k and v, the norm of queries and keys, and the
+ * selective state-space scan, a diagonal recurrence with a decay of its own
+ * per channel and state entry (gdr_chunk_fwd has one per head or key channel;
+ * "The Eraser Trilogy", the selective state-space section).
+ * Beside the file's conventions:
+ * Strides: activations may be slices of wider arrays. Their innermost axes are
+ *   dense (stated per call); the outer strides, in elements, are given in a
+ *   HOST array `strides` in the order stated (NULL: dense arrays in the layout
+ *   shown). Outputs and gradients are dense. Any strides and element-aligned
+ *   pointers are taken; 16-byte aligned ones are faster where a call says so.
+ * Lengths: `lengths` (device int32 [B], or NULL) gives each sequence's number
+ *   of tokens, held to [0, T]. Rows from there on are not read; outputs and
+ *   gradients there are 0, and the final state is the one after the last token.
+ * Types: activations have type `dtype`. Parameters of the convolution and the
+ *   norm have `weight_dtype`, which is `dtype` or GDR_FP32; the scan's A, D
+ *   and delta_bias are fp32. Gradients of outputs have `grad_dtype`, `dtype`
+ *   or GDR_FP32 (so fp32 gradients of gdr_chunk_bwd can be handed on); gradients
+ *   of inputs are fp32, written completely and deterministic (no atomics).
+ *   Sums, states and norms are fp32; an output is rounded once.
+ * Errors as for the recurrence, on the host and before any launch; a pointer
+ *   that is not element-aligned gives GDR_ERR_MISALIGNED. None of these kernels
+ *   waits on anything that another launch writes, so there is no status word.
+ */
+#define GDR_ACT_NONE 0
+#define GDR_ACT_SILU 1
+#define GDR_NORM_L2 0
+#define GDR_NORM_RMS 1
+#define GDR_ROTARY_HALF 0
+#define GDR_ROTARY_INTERLEAVED 1
+
+/*
+ * gdr_conv_fwd -- short causal depthwise convolution over whole sequences.
+ *
+ *   y_t = act(bias + sum_{j<W} weight[:, j] x_{t-W+1+j}),  act: identity or
+ *   p sigmoid(p);  X_T = the last W - 1 inputs, in order.
+ *
+ * x [B, T, D] (strides: batch, token), weight [D, W], bias [D] or NULL,
+ * X0 [B, W-1, D] the inputs before the first token or NULL (zeros), y
+ * [B, T, D], X_T [B, W-1, D] or NULL. X_T may be X0. 2 <= W <= 4
+ * (GDR_ERR_UNSUPPORTED otherwise, as for a weight type that is neither dtype
+ * nor fp32). The 16-byte form needs D a multiple of 8 (bf16) or 4 (fp32),
+ * strides likewise and 16-byte aligned arrays.
+ */
+gdr_status gdr_conv_fwd(const void* x, const void* weight, const void* bias, const void* X0,
+                        const int* lengths, void* y, void* X_T, const long long* strides, int B,
+                        int T, int D, int W, int activation, int dtype, int weight_dtype,
+                        void* stream);
+
+/*
+ * gdr_conv_bwd -- gradients of gdr_conv_fwd given dy [B, T, D] (grad_dtype)
+ * and dX_T [B, W-1, D] fp32 or NULL: dx [B, T, D], dweight [D, W], dbias [D]
+ * (NULL exactly when bias is), dX0 [B, W-1, D] or NULL (only with X0).
+ * strides: x batch, token, dy batch, token. workspace: at least
+ * gdr_conv_bwd_workspace_size() bytes, 256-byte aligned (per-chunk sums of
+ * dweight and dbias); contents on entry ignored, on exit undefined.
+ */
+gdr_status gdr_conv_bwd(const void* x, const void* weight, const void* bias, const void* X0,
+                        const int* lengths, const void* dy, const float* dX_T, float* dx,
+                        float* dweight, float* dbias, float* dX0, void* workspace,
+                        size_t workspace_bytes, const long long* strides, int B, int T, int D,
+                        int W, int activation, int dtype, int weight_dtype, int grad_dtype,
+                        void* stream);
+size_t gdr_conv_bwd_workspace_size(int B, int T, int D, int W);
+
+/*
+ * gdr_conv_step -- one token per sequence: x [B, D] (strides: batch), y
+ * [B, D]; X [B, W-1, D] is read and moved on by one row in place.
+ * y must not alias x or X. A programmatic dependent launch, like
+ * gdr_decode_step.
+ */
+gdr_status gdr_conv_step(const void* x, const void* weight, const void* bias, void* X, void* y,
+                         const long long* strides, int B, int D, int W, int activation, int dtype,
+                         int weight_dtype, void* stream);
+
+/*
+ * gdr_scan_fwd -- selective state-space scan over whole sequences.
+ *
+ *   dt = softplus(delta + delta_bias)   (delta + delta_bias without delta_softplus)
+ *   h_t[d,n] = exp(dt_t[d] A[d,n]) h_{t-1}[d,n] + dt_t[d] u_t[d] Bm_t[g,n]
+ *   y_t[d] = (sum_n Cm_t[g,n] h_t[d,n] + D[d] u_t[d]) (z_t[d] sigmoid(z_t[d]))
+ *
+ * with g = d / (D_ / G). u, delta, z [B, T, D_]; Bm, Cm [B, T, G, N] with
+ * [G, N] dense; A [D_, N] (negative for a decay; not enforced), D, delta_bias
+ * [D_] or NULL, z NULL for no gate; h0, h_T [B, D_, N] fp32 or NULL (h0 = 0 /
+ * not written), h_T may be h0; y [B, T, D_]. strides: batch and token of u,
+ * delta, Bm, Cm, z. 1 <= N <= 128, D_ a multiple of G.
+ */
+gdr_status gdr_scan_fwd(const void* u, const void* delta, const float* A, const void* Bm,
+                        const void* Cm, const float* D, const void* z, const float* delta_bias,
+                        const float* h0, const int* lengths, void* y, float* h_T,
+                        const long long* strides, int B, int T, int D_, int N, int G,
+                        int delta_softplus, int dtype, void* stream);
+
+/*
+ * gdr_scan_bwd -- gradients of gdr_scan_fwd given dy [B, T, D_] (grad_dtype)
+ * and dh_T [B, D_, N] fp32 or NULL: du, ddelta, dz [B, T, D_], dA [D_, N],
+ * dB, dC [B, T, G, N], dD, ddelta_bias [D_], dh0 [B, D_, N]; all fp32. dz, dD
+ * and ddelta_bias are NULL exactly when z, D and delta_bias are; dh0 may be
+ * NULL and needs h0. strides: as gdr_scan_fwd, then dy batch, token.
+ * workspace: at least gdr_scan_bwd_workspace_size() bytes, 256-byte aligned
+ * (the state every 8 tokens, sums of dB and dC per channel tile, sums of the
+ * parameter gradients per sequence).
+ */
+gdr_status gdr_scan_bwd(const void* u, const void* delta, const float* A, const void* Bm,
+                        const void* Cm, const float* D, const void* z, const float* delta_bias,
+                        const float* h0, const int* lengths, const void* dy, const float* dh_T,
+                        float* du, float* ddelta, float* dA, float* dB, float* dC, float* dD,
+                        float* dz, float* ddelta_bias, float* dh0, void* workspace,
+                        size_t workspace_bytes, const long long* strides, int B, int T, int D_,
+                        int N, int G, int delta_softplus, int dtype, int grad_dtype, void* stream);
+size_t gdr_scan_bwd_workspace_size(int B, int T, int D_, int N, int G);
+
+/*
+ * gdr_scan_step -- one token per sequence: u, delta, z, y [B, D_], Bm, Cm
+ * [B, G, N], h [B, D_, N] fp32 updated in place. strides: batch of u, delta,
+ * Bm, Cm, z. y must not alias an input or h. A programmatic dependent launch.
+ */
+gdr_status gdr_scan_step(const void* u, const void* delta, const float* A, const void* Bm,
+                         const void* Cm, const float* D, const void* z, const float* delta_bias,
+                         float* h, void* y, const long long* strides, int B, int D_, int N, int G,
+                         int delta_softplus, int dtype, void* stream);
+
+/*
+ * gdr_qk_norm_fwd -- norm of every query and key row, with the position
+ * rotation in the same pass.
+ *
+ *   kind GDR_NORM_L2:  n = x / max(|x|, eps)           (no weights)
+ *   kind GDR_NORM_RMS: n = weight . x / sqrt(mean(x^2) + eps)  (weight NULL: ones)
+ *   then elements [0, rot) are rotated in pairs (x1, x2) to
+ *   s (x1 cos a - x2 sin a, x2 cos a + x1 sin a), a = position * inv_freq[i],
+ *   s = rotary_scale; pair i is (i, i + rot/2) (GDR_ROTARY_HALF) or
+ *   (2i, 2i + 1) (GDR_ROTARY_INTERLEAVED); then q rows are multiplied by q_scale.
+ *
+ * q [B, T, H_q, d], k [B, T, H_k, d] (NULL with H_k = 0), weights [d],
+ * inv_freq fp32 [rot / 2] (NULL exactly when rot = 0; scale it for longer
+ * contexts), positions [B, T] int32 (int64 with position_int64 = 1), any
+ * value, or NULL for 0 .. T-1. strides: q batch, token, head, k batch, token,
+ * head, positions batch, token. q_out, k_out dense; q_out may be q where q is
+ * dense (likewise k). 1 <= d <= 256, rot even and at most d, eps > 0. Angles
+ * are reduced exactly for any position. The 16-byte form needs d a multiple of
+ * 8, strides likewise, 16-byte aligned arrays and, in the half layout, rot a
+ * multiple of 16.
+ */
+gdr_status gdr_qk_norm_fwd(const void* q, const void* k, const void* q_weight,
+                           const void* k_weight, const void* positions, const float* inv_freq,
+                           void* q_out, void* k_out, const long long* strides, int B, int T,
+                           int H_q, int H_k, int d, int rot, int kind, int rotary, float eps,
+                           float q_scale, float rotary_scale, int position_int64, int dtype,
+                           int weight_dtype, void* stream);
+
+/*
+ * gdr_qk_norm_bwd -- gradients of gdr_qk_norm_fwd given dq_out, dk_out
+ * (grad_dtype): dq, dk fp32 dense, dq_weight, dk_weight [d] (NULL exactly when
+ * the weight is). strides: as gdr_qk_norm_fwd, then dq_out batch, token, head,
+ * dk_out batch, token, head. workspace: at least
+ * gdr_qk_norm_bwd_workspace_size(d) bytes, 256-byte aligned, needed with
+ * weights only. The derivative of max(|x|, eps) is taken as 0 at and below eps.
+ */
+gdr_status gdr_qk_norm_bwd(const void* q, const void* k, const void* q_weight,
+                           const void* k_weight, const void* positions, const float* inv_freq,
+                           const void* dq_out, const void* dk_out, float* dq, float* dk,
+                           float* dq_weight, float* dk_weight, void* workspace,
+                           size_t workspace_bytes, const long long* strides, int B, int T, int H_q,
+                           int H_k, int d, int rot, int kind, int rotary, float eps, float q_scale,
+                           float rotary_scale, int position_int64, int dtype, int weight_dtype,
+                           int grad_dtype, void* stream);
+size_t gdr_qk_norm_bwd_workspace_size(int d);
+
+/*
  * gdr_selftest_bounded_wait -- diagnostic for the kernels' bounded waits.
  *
  * Launches one block that waits, with the bounded mbarrier wait used by the
