@@ -7,131 +7,174 @@
 // Backward, with dp_t = dy_t dy/dp (sigmoid(p)(1 + p(1 - sigmoid(p)))):
 //   dx_s = sum_j w_j dp_{s+W-1-j},  dw_j = sum_t dp_t x_{t-W+1+j},  dbias = sum_t dp_t.
 //
-// Bound by HBM: a token-channel is read once and written once against about
-// 2 W + 6 flops. One thread owns V adjacent channels (16-byte rows) and walks
-// `tt` tokens with the last W - 1 inputs in registers, so a row is loaded once
-// per chunk (plus W - 1 halo rows, which L2 serves); eight rows are requested
-// before the first is used. Threads are numbered with the channel vector
-// fastest, so narrow layers fill warps too. All sums are fp32; y is rounded
-// once, gradients are fp32.
+// Bound by HBM: a token-channel is read once and written once. The kernels come
+// near that only with few instructions per element (first version: 23 forward,
+// 50 backward, the issue slots 73% and 68% busy), so: a thread owns V adjacent
+// channels as packed pairs of fp32, walks `tt` tokens with the last W - 1 inputs
+// in registers (a row is loaded once per chunk, plus W - 1 halo rows that L2
+// serves), and tokens whose batch lies inside chunk and sequence take a path
+// without conditions. The rows of the next batch are on their way meanwhile.
+// Threads are numbered with the channel vector fastest, so narrow layers fill
+// warps too. All sums are fp32; y is rounded once, gradients are fp32.
 #include "layer_common.cuh"
 
 namespace gdr {
 
-constexpr int kConvBatch = 8;  // rows requested ahead of their use
+// Channels of a thread and tokens of a batch. Forward, 2 x 4096 x 8192 bf16, 4
+// taps: 4 channels and 4 tokens 56.6 us, 4 and 8 63.8, 8 and 4 60.7. Backward,
+// 4 x 4096 x 6144: 4 and 4 172 us, 4 and 2 199, 2 and 4 207.
+constexpr int kConvVec = 4, kConvAhead = 4;
 
 struct ConvShape {
     int T, D, nvec, nchunk, tt, silu, w_f32;
     unsigned total;  // threads: B * nchunk * nvec
 };
 
-// Filter taps of V channels: [D, W] row-major is V * W consecutive elements.
-template <typename T, int V, int W>
-__device__ __forceinline__ void load_taps(float (&w)[W][V], float (&bias)[V], const void* weight,
-                                          const void* bp, int c, int w_f32) {
-    float flat[V * W];
-    if (w_f32) {
-        const float* p = reinterpret_cast<const float*>(weight) + (size_t)c * W;
+// Filter taps and bias of V channels (`left` of them real).
+template <typename T, int V, int W, bool VEC>
+__device__ __forceinline__ void load_taps(f2 (&w)[W][V / 2], f2 (&bias)[V / 2], const void* weight, const void* bp,
+                                          int c, int left, int w_f32) {
+    float flat[V * W], bf[V];  // [V][W], as the rows of [D, W] lie
+    if (VEC && w_f32) {
 #pragma unroll
-        for (int i = 0; i < V * W; i += (V > 1 ? 4 : 1)) VecIO<float, (V > 1 ? 4 : 1)>::load(flat + i, p + i);
+        for (int i = 0; i < V * W; i += 4)
+            VecIO<float, 4>::load(flat + i, reinterpret_cast<const float*>(weight) + (size_t)c * W + i);
+    } else if (VEC) {
+#pragma unroll
+        for (int i = 0; i < V * W; i += V)
+            VecIO<T, V>::load(flat + i, reinterpret_cast<const T*>(weight) + (size_t)c * W + i);
     } else {
-        const T* p = reinterpret_cast<const T*>(weight) + (size_t)c * W;
 #pragma unroll
-        for (int i = 0; i < V * W; i += V) VecIO<T, V>::load(flat + i, p + i);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = flat[i * W + j];
+        for (int i = 0; i < V * W; ++i)
+            flat[i] = i >= left * W ? 0.f
+                      : w_f32 ? reinterpret_cast<const float*>(weight)[(size_t)c * W + i]
+                              : to_f32(reinterpret_cast<const T*>(weight)[(size_t)c * W + i]);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        bias[i] = !bp ? 0.f
-                  : w_f32 ? reinterpret_cast<const float*>(bp)[c + i]
-                          : to_f32(reinterpret_cast<const T*>(bp)[c + i]);
-}
-
-// Input row r of sequence b (r >= -(W-1); negative rows come from X0).
-template <typename T, int V, int W>
-__device__ __forceinline__ void load_row(float* f, const T* xb, const T* X0b, long long xt, int D, int r) {
-    if (r >= 0) {
-        VecIO<T, V>::load(f, xb + r * xt);
-    } else if (X0b) {
-        VecIO<T, V>::load(f, X0b + (size_t)(r + W - 1) * D);
-    } else {
+        bf[i] = !bp || i >= left ? 0.f
+                : w_f32 ? reinterpret_cast<const float*>(bp)[c + i]
+                        : to_f32(reinterpret_cast<const T*>(bp)[c + i]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = 0.f;
+    for (int i = 0; i < V / 2; ++i) {
+        bias[i] = pack2(bf[2 * i], bf[2 * i + 1]);
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][i] = pack2(flat[2 * i * W + j], flat[(2 * i + 1) * W + j]);
     }
 }
 
-template <typename T, int V, int W>
+// The W - 1 inputs before row t0 of a sequence of n tokens (negative rows come
+// from X0); rows from n on are not read.
+template <typename T, int V, int W, bool VEC>
+__device__ __forceinline__ void load_window(f2 (&win)[W][V / 2], const T* xr, const T* X0r, long long xt, int D, int t0,
+                                            int n, int left) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int r = t0 - (W - 1) + j;
+        RowIO<T, V, VEC> row;
+        row.zero();
+        if (r >= 0 && r < n) row.load(xr + r * xt, left);
+        else if (r < 0 && X0r) row.load(X0r + (size_t)(r + W - 1) * D, left);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) win[j][i] = row.pair(i);
+    }
+}
+
+template <int P, int W> __device__ __forceinline__ void slide(f2 (&win)[W][P]) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int i = 0; i < P; ++i) win[j][i] = win[j + 1][i];
+}
+
+template <typename T, int V, int W, bool VEC>
 __global__ void __launch_bounds__(128) conv_fwd_kernel(const T* __restrict__ x, const void* __restrict__ weight,
                                                        const void* __restrict__ bias, const T* X0,
                                                        const int* __restrict__ lengths, T* __restrict__ y, T* X_T,
                                                        long long xb, long long xt, ConvShape s) {
+    constexpr int P = V / 2, K = kConvAhead;
+    using Row = RowIO<T, V, VEC>;
     const unsigned idx = blockIdx.x * 128u + threadIdx.x;
     if (idx >= s.total) return;
     const unsigned r0 = idx / s.nvec;
-    const int c = (idx - r0 * s.nvec) * V;
+    const int c = (idx - r0 * s.nvec) * V, left = s.D - c;
     const int b = r0 / s.nchunk, chunk = r0 - b * s.nchunk;
     const int t0 = chunk * s.tt, t1 = min(s.T, t0 + s.tt);
     const int n = seq_len(lengths, b, s.T);
     const T* xr = x + b * xb + c;
     const T* X0r = X0 ? X0 + (size_t)b * (W - 1) * s.D + c : nullptr;
-    T* yr = y + (size_t)b * s.T * s.D + c;
+    T* yr = y + ((size_t)b * s.T + t0) * s.D + c;
 
-    float w[W][V], bs[V], win[W][V];  // win[j]: row t - W + 1 + j
-    load_taps<T, V, W>(w, bs, weight, bias, c, s.w_f32);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const int r = t0 - (W - 1) + j;
-        if (r < n) load_row<T, V, W>(win[j], xr, X0r, xt, s.D, r);
-        else
-#pragma unroll
-            for (int i = 0; i < V; ++i) win[j][i] = 0.f;
-    }
+    f2 w[W][P], bs[P], win[W][P];  // win[j]: row t - W + 1 + j
+    load_taps<T, V, W, VEC>(w, bs, weight, bias, c, left, s.w_f32);
+    load_window<T, V, W, VEC>(win, xr, X0r, xt, s.D, t0, n, left);
     // The first chunk writes the carried rows. X_T may be X0 itself: only this
     // thread reads these channels of X0, and win holds them all by now.
     if (chunk == 0 && X_T) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const int r = n - (W - 1) + j;
-            float f[V];
-            if (r >= 0) VecIO<T, V>::load(f, xr + r * xt);
-            else
+            f2 f[P];
+            if (r >= 0) {
+                Row row;
+                row.load(xr + r * xt, left);
 #pragma unroll
-                for (int jj = 0; jj < W - 1; ++jj)
+                for (int i = 0; i < P; ++i) f[i] = row.pair(i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < P; ++i) f[i] = win[0][i];
+#pragma unroll
+                for (int jj = 1; jj < W - 1; ++jj)
                     if (r + W - 1 == jj)
 #pragma unroll
-                        for (int i = 0; i < V; ++i) f[i] = win[jj][i];
-            VecIO<T, V>::store(X_T + ((size_t)b * (W - 1) + j) * s.D + c, f);
+                        for (int i = 0; i < P; ++i) f[i] = win[jj][i];
+            }
+            Row::store(X_T + ((size_t)b * (W - 1) + j) * s.D + c, f, left);
         }
     }
-    for (int tb = t0; tb < t1; tb += kConvBatch) {
-        float rows[kConvBatch][V];
+    const int end = min(t1, n);
+    Row next[K];
+    const T* xp = xr + t0 * xt;
 #pragma unroll
-        for (int k = 0; k < kConvBatch; ++k) {
-            if (tb + k < min(t1, n)) VecIO<T, V>::load(rows[k], xr + (tb + k) * xt);
-            else
+    for (int k = 0; k < K; ++k) {
+        next[k].zero();
+        if (t0 + k < end) next[k].load(xp + k * xt, left);
+    }
+    for (int tb = t0; tb < t1; tb += K) {
+        Row rows[K];
+        xp += K * xt;
 #pragma unroll
-                for (int i = 0; i < V; ++i) rows[k][i] = 0.f;
+        for (int k = 0; k < K; ++k) rows[k] = next[k];
+        if (tb + 2 * K <= end) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) next[k].load(xp + k * xt, left);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (tb + K + k < end) next[k].load(xp + k * xt, left);
         }
+        const bool whole = tb + K <= end;
 #pragma unroll
-        for (int k = 0; k < kConvBatch; ++k) {
-            const int t = tb + k;
-            if (t >= t1) break;
-            float out[V];
+        for (int k = 0; k < K; ++k) {
+            f2 out[P];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                win[W - 1][i] = rows[k][i];
-                float p = bs[i];
+            for (int i = 0; i < P; ++i) {
+                win[W - 1][i] = rows[k].pair(i);
+                out[i] = bs[i];
 #pragma unroll
-                for (int j = 0; j < W; ++j) p = fmaf(w[j][i], win[j][i], p);
-                out[i] = t >= n ? 0.f : s.silu ? p * sigmoidf_fast(p) : p;
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
+                for (int j = 0; j < W; ++j) out[i] = fma2(w[j][i], win[j][i], out[i]);
             }
-            VecIO<T, V>::store(yr + (size_t)t * s.D, out);
+            if (s.silu) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) out[i] = mul2(out[i], sigmoid2(out[i]));
+            }
+            slide(win);
+            if (!whole && tb + k >= n) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) out[i] = both2(0.f);
+            }
+            if (whole || tb + k < t1) Row::store(yr, out, left);
+            yr += s.D;
         }
     }
 }
@@ -139,100 +182,154 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const T* __restrict__ x, 
 // One chunk of tokens: dx of its rows (and dX0 in the first chunk), and the
 // chunk's partial dw, dbias. dx_s needs dp up to W - 1 tokens on, so the walk
 // runs W - 1 tokens past the chunk; those tokens' dw belongs to the next chunk.
-template <typename T, typename TG, int V, int W>
+template <typename T, typename TG, int V, int W, bool VEC>
 __global__ void __launch_bounds__(128) conv_bwd_kernel(
     const T* __restrict__ x, const void* __restrict__ weight, const void* __restrict__ bias,
     const T* __restrict__ X0, const int* __restrict__ lengths, const TG* __restrict__ dy,
     const float* __restrict__ dX_T, float* __restrict__ dx, float* __restrict__ dX0, float* __restrict__ part,
     long long xb, long long xt, long long gb, long long gt, ConvShape s) {
+    constexpr int P = V / 2, K = kConvAhead;
+    using Row = RowIO<T, V, VEC>;
+    using Grad = RowIO<TG, V, VEC>;
+    using Out = RowIO<float, V, VEC>;
     const unsigned idx = blockIdx.x * 128u + threadIdx.x;
     if (idx >= s.total) return;
     const unsigned r0 = idx / s.nvec;
-    const int c = (idx - r0 * s.nvec) * V;
+    const int c = (idx - r0 * s.nvec) * V, left = s.D - c;
     const int b = r0 / s.nchunk, chunk = r0 - b * s.nchunk;
-    const int t0 = chunk * s.tt, t1 = min(s.T, t0 + s.tt);
+    const int t0 = chunk * s.tt, t1 = min(s.T, t0 + s.tt), stop = t1 + W - 1;
     const int n = seq_len(lengths, b, s.T);
     const T* xr = x + b * xb + c;
-    const TG* gr = dy + b * gb + c;
     const T* X0r = X0 ? X0 + (size_t)b * (W - 1) * s.D + c : nullptr;
 
-    float w[W][V], bs[V], win[W][V], dw[W][V], db[V], acc[W][V];
-    load_taps<T, V, W>(w, bs, weight, bias, c, s.w_f32);
+    f2 w[W][P], bs[P], win[W][P], dw[W][P], db[P], acc[W][P];  // acc[j]: dx of row t - W + 1 + j so far
+    load_taps<T, V, W, VEC>(w, bs, weight, bias, c, left, s.w_f32);
+    load_window<T, V, W, VEC>(win, xr, X0r, xt, s.D, t0, n, left);
 #pragma unroll
-    for (int j = 0; j < W; ++j)
+    for (int i = 0; i < P; ++i) {
+        db[i] = both2(0.f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dw[j][i] = acc[j][i] = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) db[i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const int r = t0 - (W - 1) + j;
-        if (r < n) load_row<T, V, W>(win[j], xr, X0r, xt, s.D, r);
-        else
-#pragma unroll
-            for (int i = 0; i < V; ++i) win[j][i] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j][i] = acc[j][i] = both2(0.f);
     }
-    for (int tb = t0; tb < t1 + W - 1; tb += kConvBatch) {
-        float rows[kConvBatch][V], grads[kConvBatch][V];
+    // one token: dp from its row and gradient, its share of the sums (SUM), and
+    // the gradient of row t - W + 1, complete after it
+    auto token = [&](const Row& row, const Grad& grad, bool sum, f2 (&out)[P]) {
 #pragma unroll
-        for (int k = 0; k < kConvBatch; ++k) {
-            if (tb + k < min(t1 + W - 1, n)) {
-                VecIO<T, V>::load(rows[k], xr + (tb + k) * xt);
-                VecIO<TG, V>::load(grads[k], gr + (tb + k) * gt);
-            } else {
+        for (int i = 0; i < P; ++i) {
+            win[W - 1][i] = row.pair(i);
+            f2 dp = grad.pair(i);
+            if (s.silu) {
+                f2 p = bs[i];
 #pragma unroll
-                for (int i = 0; i < V; ++i) rows[k][i] = grads[k][i] = 0.f;
+                for (int j = 0; j < W; ++j) p = fma2(w[j][i], win[j][i], p);
+                const f2 sg = sigmoid2(p);
+                // sg (1 + p (1 - sg))
+                dp = mul2(dp, mul2(sg, fma2(p, fma2(sg, both2(-1.f), both2(1.f)), both2(1.f))));
+            }
+            if (sum) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) dw[j][i] = fma2(dp, win[j][i], dw[j][i]);
+                db[i] = add2(db[i], dp);
+            }
+            out[i] = fma2(w[0][i], dp, acc[0][i]);
+#pragma unroll
+            for (int j = 1; j < W; ++j) acc[j - 1][i] = j < W - 1 ? fma2(w[j][i], dp, acc[j][i]) : mul2(w[j][i], dp);
+        }
+        slide(win);
+    };
+    const int end = min(stop, n);  // tokens from here on are not read
+    Row xnext[K];
+    Grad gnext[K];
+    const T* xp = xr + t0 * xt;
+    const TG* gp = dy + b * gb + c + t0 * gt;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        xnext[k].zero();
+        gnext[k].zero();
+        if (t0 + k < end) {
+            xnext[k].load(xp + k * xt, left);
+            gnext[k].load(gp + k * gt, left);
+        }
+    }
+    float* dxr = dx + ((long long)b * s.T + t0 - (W - 1)) * s.D + c;  // row t - W + 1
+    for (int tb = t0; tb < stop; tb += K) {
+        Row rows[K];
+        Grad grads[K];
+        xp += K * xt;
+        gp += K * gt;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            rows[k] = xnext[k];
+            grads[k] = gnext[k];
+        }
+        if (tb + 2 * K <= end) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                xnext[k].load(xp + k * xt, left);
+                gnext[k].load(gp + k * gt, left);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                xnext[k].zero();
+                gnext[k].zero();
+                if (tb + K + k < end) {
+                    xnext[k].load(xp + k * xt, left);
+                    gnext[k].load(gp + k * gt, left);
+                }
             }
         }
+        if (tb >= t0 + W - 1 && tb + K <= min(t1, n)) {
 #pragma unroll
-        for (int k = 0; k < kConvBatch; ++k) {
-            const int t = tb + k;
-            if (t >= t1 + W - 1) break;
-            const int e = t - (W - 1);  // the row whose gradient is complete after this token
-            float out[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                win[W - 1][i] = rows[k][i];
-                float dp = grads[k][i];  // 0 from n on
-                if (s.silu) {
-                    float p = bs[i];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) p = fmaf(w[j][i], win[j][i], p);
-                    const float sg = sigmoidf_fast(p);
-                    dp = t < n ? dp * (sg * fmaf(p, 1.f - sg, 1.f)) : 0.f;
-                }
-                if (t < t1) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][i] = fmaf(dp, win[j][i], dw[j][i]);
-                    db[i] += dp;
-                }
-#pragma unroll
-                for (int j = 0; j < W; ++j) acc[j][i] = fmaf(w[j][i], dp, acc[j][i]);
-                out[i] = acc[0][i];
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) {
-                    acc[j][i] = acc[j + 1][i];
-                    win[j][i] = win[j + 1][i];
-                }
-                acc[W - 1][i] = 0.f;
+            for (int k = 0; k < K; ++k) {
+                f2 out[P];
+                token(rows[k], grads[k], true, out);
+                Out::store(dxr, out, left);
+                dxr += s.D;
             }
-            const bool lead = chunk == 0 && e < 0;  // a carried row
-            if (e < t0 && !lead) continue;
-            const int tail = e - (n - (W - 1));  // row of X_T that is input row e
-            if (dX_T && tail >= 0 && tail < W - 1) {
-                float f[V];
-                VecIO<float, V>::load(f, dX_T + ((size_t)b * (W - 1) + tail) * s.D + c);
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < K; ++k) {
+                const int t = tb + k, e = t - (W - 1);
+                Row row = rows[0];  // rows[k] without an index that is not constant
+                Grad grad = grads[0];
 #pragma unroll
-                for (int i = 0; i < V; ++i) out[i] += f[i];
+                for (int q = 1; q < K; ++q)
+                    if (q == k) { row = rows[q]; grad = grads[q]; }
+                f2 out[P];
+                // a token that is not read has dp = 0: its gradient is 0 and, its
+                // window being finite, so is dy/dp times it
+                if (t >= n) {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        out[i] = acc[0][i];
+#pragma unroll
+                        for (int j = 1; j < W; ++j) acc[j - 1][i] = j < W - 1 ? acc[j][i] : both2(0.f);
+                    }
+                    slide(win);
+                } else {
+                    token(row, grad, t < t1, out);
+                }
+                const bool lead = chunk == 0 && e < 0;  // a carried row
+                const int tail = e - (n - (W - 1));     // row of X_T that is input row e
+                if (t < stop && (e >= t0 || lead)) {
+                    if (dX_T && tail >= 0 && tail < W - 1) {
+                        Out d;
+                        d.load(dX_T + ((size_t)b * (W - 1) + tail) * s.D + c, left);
+#pragma unroll
+                        for (int i = 0; i < P; ++i) out[i] = add2(out[i], d.pair(i));
+                    }
+                    if (!lead) Out::store(dxr, out, left);
+                    else if (dX0) Out::store(dX0 + ((size_t)b * (W - 1) + e + W - 1) * s.D + c, out, left);
+                }
+                dxr += s.D;
             }
-            if (!lead) VecIO<float, V>::store(dx + ((size_t)b * s.T + e) * s.D + c, out);
-            else if (dX0) VecIO<float, V>::store(dX0 + ((size_t)b * (W - 1) + e + W - 1) * s.D + c, out);
         }
     }
     float* pr = part + (size_t)r0 * (W + 1) * s.D + c;  // partial sums [b, chunk][W + 1][D]
 #pragma unroll
-    for (int j = 0; j < W; ++j) VecIO<float, V>::store(pr + (size_t)j * s.D, dw[j]);
-    VecIO<float, V>::store(pr + (size_t)W * s.D, db);
+    for (int j = 0; j < W; ++j) Out::store(pr + (size_t)j * s.D, dw[j], left);
+    Out::store(pr + (size_t)W * s.D, db, left);
 }
 
 // dweight [D, W] and dbias [D] from `parts` partials of [W + 1][D]: 32 columns
@@ -258,37 +355,48 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(const float* __restric
     }
 }
 
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool VEC>
 __global__ void __launch_bounds__(128) conv_step_kernel(const T* __restrict__ x, const void* __restrict__ weight,
                                                         const void* __restrict__ bias, T* __restrict__ X,
                                                         T* __restrict__ y, long long xb, ConvShape s) {
+    constexpr int P = V / 2;
+    using Row = RowIO<T, V, VEC>;
     dependent_launch();
     const unsigned idx = blockIdx.x * 128u + threadIdx.x;
     if (idx >= s.total) return;
     const int b = idx / s.nvec;
-    const int c = (idx - b * s.nvec) * V;
-    float w[W][V], bs[V], win[W][V], out[V];
+    const int c = (idx - b * s.nvec) * V, left = s.D - c;
+    f2 w[W][P], bs[P];
+    Row rows[W];
     dependent_wait();
     T* Xr = X + (size_t)b * (W - 1) * s.D + c;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) VecIO<T, V>::load(win[j], Xr + (size_t)j * s.D);
-    VecIO<T, V>::load(win[W - 1], x + b * xb + c);
-    load_taps<T, V, W>(w, bs, weight, bias, c, s.w_f32);
+    for (int j = 0; j < W - 1; ++j) rows[j].load(Xr + (size_t)j * s.D, left);
+    rows[W - 1].load(x + b * xb + c, left);
+    load_taps<T, V, W, VEC>(w, bs, weight, bias, c, left, s.w_f32);
+    f2 out[P];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float p = bs[i];
+    for (int i = 0; i < P; ++i) {
+        out[i] = bs[i];
 #pragma unroll
-        for (int j = 0; j < W; ++j) p = fmaf(w[j][i], win[j][i], p);
-        out[i] = s.silu ? p * sigmoidf_fast(p) : p;
+        for (int j = 0; j < W; ++j) out[i] = fma2(w[j][i], rows[j].pair(i), out[i]);
+        if (s.silu) out[i] = mul2(out[i], sigmoid2(out[i]));
     }
-    VecIO<T, V>::store(y + (size_t)b * s.D + c, out);
+    Row::store(y + (size_t)b * s.D + c, out, left);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) VecIO<T, V>::store(Xr + (size_t)j * s.D, win[j + 1]);
+    for (int j = 0; j < W - 1; ++j) {
+        f2 f[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) f[i] = rows[j + 1].pair(i);
+        Row::store(Xr + (size_t)j * s.D, f, left);
+    }
 }
 
 // Tokens per thread. A chunk of tt tokens loads W - 1 halo rows and writes one
-// set of partials, so longer is better until there are too few threads to keep
-// the loads in flight; `want` threads fill the card.
+// set of partials, so longer is better (forward of the case above: 32 tokens
+// 59.7 us, 64 and 128 56.6; backward: 64 tokens 188 us, 128 184, 256 172) until
+// there are too few threads to keep the loads in flight; `want` threads fill
+// the card.
 static int conv_tokens(long long per_token, int T, int lo, int hi, long long want) {
     int tt = hi;
     while (tt > lo && per_token * ((T + tt - 1) / tt) < want) tt /= 2;
@@ -296,11 +404,12 @@ static int conv_tokens(long long per_token, int T, int lo, int hi, long long wan
 }
 
 static int conv_fwd_tokens(int B, int T, int nvec) {
-    return conv_tokens((long long)B * nvec, T, 8, 32, 148 * 2048);
+    return conv_tokens((long long)B * nvec, T, 8, 64, 148 * 1024);
 }
 static int conv_bwd_tokens(int B, int T, int nvec) {
-    return conv_tokens((long long)B * nvec, T, 16, 128, 148 * 1024);
+    return conv_tokens((long long)B * nvec, T, 16, 256, 148 * 512);
 }
+static int conv_vectors(int D) { return (D + kConvVec - 1) / kConvVec; }
 static int conv_chunks(int T, int tt) { return T > 0 ? (T + tt - 1) / tt : 1; }
 
 template <typename F> static bool dispatch_taps(int W, F&& f) {
@@ -328,15 +437,15 @@ static gdr_status conv_check(const void* weight, const void* bias, int B, int T,
     return GDR_OK;
 }
 
-// 16-byte rows: the channel count and every stride a multiple of the vector,
+// Wide loads: the channel count and every stride a multiple of the vector,
 // every pointer aligned to it.
-static bool conv_vector(int D, int V, size_t e, const void* weight, std::initializer_list<const void*> ptrs,
+static bool conv_vector(int D, size_t e, const void* weight, std::initializer_list<const void*> ptrs,
                         std::initializer_list<long long> strides) {
-    if (D % V || !aligned_to(weight, 16)) return false;
+    if (D % kConvVec || !aligned_to(weight, 16)) return false;
     for (const void* p : ptrs)
-        if (!aligned_to(p, e * V < 16 ? e * V : 16)) return false;
+        if (!aligned_to(p, e * kConvVec)) return false;
     for (long long st : strides)
-        if (st % V) return false;
+        if (st % kConvVec) return false;
     return true;
 }
 
@@ -355,10 +464,9 @@ gdr_status gdr_conv_fwd(const void* x, const void* weight, const void* bias, con
         if (!aligned_to(p, e)) return GDR_ERR_MISALIGNED;
     if (!aligned_to(lengths, 4)) return GDR_ERR_MISALIGNED;
     const long long xb = strides ? strides[0] : (long long)T * D, xt = strides ? strides[1] : D;
-    const int V = dtype == GDR_BF16 ? 8 : 4;
-    const bool vec = conv_vector(D, V, e, weight, {x, X0, y, X_T}, {xb, xt});
+    const bool vec = conv_vector(D, e, weight, {x, X0, y, X_T}, {xb, xt});
     ConvShape s = {};
-    s.T = T; s.D = D; s.nvec = vec ? D / V : D;
+    s.T = T; s.D = D; s.nvec = conv_vectors(D);
     s.tt = conv_fwd_tokens(B, T, s.nvec);
     s.nchunk = conv_chunks(T, s.tt);
     s.silu = activation == GDR_ACT_SILU;
@@ -370,11 +478,14 @@ gdr_status gdr_conv_fwd(const void* x, const void* weight, const void* bias, con
     cudaStream_t st = as_stream(stream);
     dispatch_taps(W, [&](auto wc) {
         constexpr int WT = decltype(wc)::value;
-#define GDR_CONV_FWD(TT, VV)                                                                              \
-    conv_fwd_kernel<TT, VV, WT><<<grid, 128, 0, st>>>((const TT*)x, weight, bias, (const TT*)X0, lengths, \
+#define GDR_CONV_FWD(TT, VEC)                                                                             \
+    conv_fwd_kernel<TT, kConvVec, WT, VEC><<<grid, 128, 0, st>>>((const TT*)x, weight, bias, (const TT*)X0, lengths, \
                                                       (TT*)y, (TT*)X_T, xb, xt, s)
-        if (dtype == GDR_BF16) { if (vec) GDR_CONV_FWD(__nv_bfloat16, 8); else GDR_CONV_FWD(__nv_bfloat16, 1); }
-        else { if (vec) GDR_CONV_FWD(float, 4); else GDR_CONV_FWD(float, 1); }
+        if (dtype == GDR_BF16) {
+            if (vec) GDR_CONV_FWD(__nv_bfloat16, true); else GDR_CONV_FWD(__nv_bfloat16, false);
+        } else {
+            if (vec) GDR_CONV_FWD(float, true); else GDR_CONV_FWD(float, false);
+        }
 #undef GDR_CONV_FWD
     });
     return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
@@ -382,8 +493,7 @@ gdr_status gdr_conv_fwd(const void* x, const void* weight, const void* bias, con
 
 size_t gdr_conv_bwd_workspace_size(int B, int T, int D, int W) {
     if (B < 1 || T < 0 || D < 1 || W < 2 || W > 4) return 0;
-    // the narrow form (one channel per thread) has at most as many chunks
-    const int tt = conv_bwd_tokens(B, T, D % 4 ? D : D / 4);
+    const int tt = conv_bwd_tokens(B, T, conv_vectors(D));
     return round256((size_t)B * conv_chunks(T, tt) * (W + 1) * D * sizeof(float));
 }
 
@@ -406,12 +516,12 @@ gdr_status gdr_conv_bwd(const void* x, const void* weight, const void* bias, con
         if (!aligned_to(p, 4)) return GDR_ERR_MISALIGNED;
     const long long xb = strides ? strides[0] : (long long)T * D, xt = strides ? strides[1] : D;
     const long long gb = strides ? strides[2] : (long long)T * D, gt = strides ? strides[3] : D;
-    const bool vec = conv_vector(D, 4, e, weight, {x, X0}, {xb, xt, gb, gt}) && aligned_to(dy, eg * 4) &&
-                     aligned_to(dX_T, 16) && aligned_to(dx, 16) && aligned_to(dX0, 16);
+    const bool vec = conv_vector(D, e, weight, {x, X0}, {xb, xt, gb, gt}) &&
+                     aligned_to(dy, eg * kConvVec) && aligned_to(dX_T, 4 * kConvVec) && aligned_to(dx, 4 * kConvVec) &&
+                     aligned_to(dX0, 4 * kConvVec);
     ConvShape s = {};
-    s.T = T; s.D = D; s.nvec = vec ? D / 4 : D;
-    // chunks of the vector form whichever runs, so that one workspace size holds
-    s.tt = conv_bwd_tokens(B, T, D % 4 ? D : D / 4);
+    s.T = T; s.D = D; s.nvec = conv_vectors(D);
+    s.tt = conv_bwd_tokens(B, T, s.nvec);
     s.nchunk = conv_chunks(T, s.tt);
     s.silu = activation == GDR_ACT_SILU;
     s.w_f32 = weight_dtype == GDR_FP32;
@@ -423,15 +533,15 @@ gdr_status gdr_conv_bwd(const void* x, const void* weight, const void* bias, con
     float* part = reinterpret_cast<float*>(workspace);
     dispatch_taps(W, [&](auto wc) {
         constexpr int WT = decltype(wc)::value;
-#define GDR_CONV_BWD(TT, TG, VV)                                                                               \
-    conv_bwd_kernel<TT, TG, VV, WT><<<grid, 128, 0, st>>>((const TT*)x, weight, bias, (const TT*)X0, lengths, \
+#define GDR_CONV_BWD(TT, TG, VEC)                                                                              \
+    conv_bwd_kernel<TT, TG, kConvVec, WT, VEC><<<grid, 128, 0, st>>>((const TT*)x, weight, bias, (const TT*)X0, lengths, \
                                                           (const TG*)dy, dX_T, dx, dX0, part, xb, xt, gb, gt, s)
-        if (dtype == GDR_FP32) { if (vec) GDR_CONV_BWD(float, float, 4); else GDR_CONV_BWD(float, float, 1); }
+        if (dtype == GDR_FP32) { if (vec) GDR_CONV_BWD(float, float, true); else GDR_CONV_BWD(float, float, false); }
         else if (grad_dtype == GDR_FP32) {
-            if (vec) GDR_CONV_BWD(__nv_bfloat16, float, 4); else GDR_CONV_BWD(__nv_bfloat16, float, 1);
+            if (vec) GDR_CONV_BWD(__nv_bfloat16, float, true); else GDR_CONV_BWD(__nv_bfloat16, float, false);
         } else {
-            if (vec) GDR_CONV_BWD(__nv_bfloat16, __nv_bfloat16, 4);
-            else GDR_CONV_BWD(__nv_bfloat16, __nv_bfloat16, 1);
+            if (vec) GDR_CONV_BWD(__nv_bfloat16, __nv_bfloat16, true);
+            else GDR_CONV_BWD(__nv_bfloat16, __nv_bfloat16, false);
         }
 #undef GDR_CONV_BWD
     });
@@ -450,10 +560,9 @@ gdr_status gdr_conv_step(const void* x, const void* weight, const void* bias, vo
     const size_t e = dtype_size(dtype);
     if (!aligned_to(x, e) || !aligned_to(X, e) || !aligned_to(y, e)) return GDR_ERR_MISALIGNED;
     const long long xb = strides ? strides[0] : D;
-    const int V = dtype == GDR_BF16 ? 8 : 4;
-    const bool vec = conv_vector(D, V, e, weight, {x, X, y}, {xb});
+    const bool vec = conv_vector(D, e, weight, {x, X, y}, {xb});
     ConvShape s = {};
-    s.T = 1; s.D = D; s.nvec = vec ? D / V : D;
+    s.T = 1; s.D = D; s.nvec = conv_vectors(D);
     s.silu = activation == GDR_ACT_SILU;
     s.w_f32 = weight_dtype == GDR_FP32;
     const long long total = (long long)B * s.nvec;
@@ -464,11 +573,14 @@ gdr_status gdr_conv_step(const void* x, const void* weight, const void* bias, vo
     cudaError_t err = cudaErrorInvalidValue;
     dispatch_taps(W, [&](auto wc) {
         constexpr int WT = decltype(wc)::value;
-#define GDR_CONV_STEP(TT, VV)                                                                       \
-    err = launch_dependent(conv_step_kernel<TT, VV, WT>, grid, 128, 0, st, (const TT*)x, weight,    \
+#define GDR_CONV_STEP(TT, VEC)                                                                      \
+    err = launch_dependent(conv_step_kernel<TT, kConvVec, WT, VEC>, grid, 128, 0, st, (const TT*)x, weight,    \
                            bias, (TT*)X, (TT*)y, xb, s)
-        if (dtype == GDR_BF16) { if (vec) GDR_CONV_STEP(__nv_bfloat16, 8); else GDR_CONV_STEP(__nv_bfloat16, 1); }
-        else { if (vec) GDR_CONV_STEP(float, 4); else GDR_CONV_STEP(float, 1); }
+        if (dtype == GDR_BF16) {
+            if (vec) GDR_CONV_STEP(__nv_bfloat16, true); else GDR_CONV_STEP(__nv_bfloat16, false);
+        } else {
+            if (vec) GDR_CONV_STEP(float, true); else GDR_CONV_STEP(float, false);
+        }
 #undef GDR_CONV_STEP
     });
     return err == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;

@@ -14,6 +14,15 @@ template <typename T> struct VecIO<T, 1> {
     static __device__ __forceinline__ void load(float* f, const T* p) { f[0] = to_f32(*p); }
     static __device__ __forceinline__ void store(T* p, const float* f) { *p = from_f32<T>(f[0]); }
 };
+template <> struct VecIO<float, 2> {
+    static __device__ __forceinline__ void load(float* f, const float* p) {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        f[0] = v.x; f[1] = v.y;
+    }
+    static __device__ __forceinline__ void store(float* p, const float* f) {
+        *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+    }
+};
 template <> struct VecIO<float, 4> {
     static __device__ __forceinline__ void load(float* f, const float* p) {
         const float4 v = *reinterpret_cast<const float4*>(p);
@@ -37,6 +46,14 @@ __device__ __forceinline__ void unpack_bf16x2(uint32_t u, float& lo, float& hi) 
     lo = __uint_as_float(u << 16);
     hi = __uint_as_float(u & 0xffff0000u);
 }
+template <> struct VecIO<__nv_bfloat16, 2> {
+    static __device__ __forceinline__ void load(float* f, const __nv_bfloat16* p) {
+        unpack_bf16x2(*reinterpret_cast<const uint32_t*>(p), f[0], f[1]);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(f[0], f[1]);
+    }
+};
 template <> struct VecIO<__nv_bfloat16, 4> {
     static __device__ __forceinline__ void load(float* f, const __nv_bfloat16* p) {
         const uint2 u = *reinterpret_cast<const uint2*>(p);
@@ -61,12 +78,102 @@ template <> struct VecIO<__nv_bfloat16, 8> {
     }
 };
 
+// V consecutive elements as loaded, so that rows requested ahead of their use
+// cost no more registers than their bytes.
+template <typename T, int V> struct RawVec {
+    static constexpr int kWords = V * sizeof(T) >= 4 ? V * sizeof(T) / 4 : 1;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (V * sizeof(T) == 2) {
+            w[0] = *reinterpret_cast<const unsigned short*>(p);
+        } else if constexpr (kWords == 1) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else if constexpr (kWords == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            w[0] = v.x; w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void set(int i, T x) {  // into zeros
+        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(x);
+        else w[i / 2] |= (uint32_t)__bfloat16_as_ushort(x) << (i % 2 * 16);
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+};
+
 constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float rsqrt_approx(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // 1 / (1 + e^-x) from the hardware exponential and reciprocal; e^-x = inf
 // gives 0. Relative error a few 2^-23 (the exponent's argument is rounded once).
 __device__ __forceinline__ float sigmoidf_fast(float x) {
-    return __fdividef(1.f, 1.f + ex2_approx(-x * kLog2e));
+    return rcp_approx(1.f + ex2_approx(-x * kLog2e));
+}
+
+// ---- packed pairs of fp32 (one instruction for two multiply-adds) ----
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 ex2_pair(f2 v) {
+    float a, b;
+    unpack2(v, a, b);
+    return pack2(ex2_approx(a), ex2_approx(b));
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    float a, b;
+    unpack2(v, a, b);
+    return a + b;
+}
+__device__ __forceinline__ f2 both2(float a) { return pack2(a, a); }
+__device__ __forceinline__ f2 sigmoid2(f2 x) {  // sigmoidf_fast of each
+    const f2 q = add2(ex2_pair(mul2(x, both2(-kLog2e))), both2(1.f));
+    float a, b;
+    unpack2(q, a, b);
+    return pack2(rcp_approx(a), rcp_approx(b));
 }
 
 // log(1 + e^x) = max(x, 0) + log1p(e^-|x|). With y = e^-|x| in (0, 1] and
@@ -75,7 +182,7 @@ __device__ __forceinline__ float sigmoidf_fast(float x) {
 // loses. Terms up to s^14: the first one dropped, s^16 / 17, is below 2^-29.
 __device__ __forceinline__ float softplusf_series(float x) {
     const float y = ex2_approx(-fabsf(x) * kLog2e);
-    const float s = __fdividef(y, 2.f + y), s2 = s * s;
+    const float s = y * rcp_approx(2.f + y), s2 = s * s;
     float r = 1.f / 15.f;
     r = fmaf(r, s2, 1.f / 13.f);
     r = fmaf(r, s2, 1.f / 11.f);
@@ -86,6 +193,36 @@ __device__ __forceinline__ float softplusf_series(float x) {
     r = fmaf(r, s2, 1.f);
     return fmaxf(x, 0.f) + 2.f * s * r;
 }
+
+// V channels (even) of one row, as loaded: wide loads (VEC), or one element at
+// a time where c + i < the row's length (`left` elements), others 0.
+template <typename T, int V, bool VEC> struct RowIO {
+    RawVec<T, V> v;
+    __device__ __forceinline__ void zero() { v.zero(); }
+    __device__ __forceinline__ void load(const T* p, int left) {
+        if constexpr (VEC) {
+            v.load(p);
+        } else {
+            v.zero();
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < left) v.set(i, p[i]);
+        }
+    }
+    __device__ __forceinline__ f2 pair(int i) const { return pack2(v.get(2 * i), v.get(2 * i + 1)); }
+    static __device__ __forceinline__ void store(T* p, const f2 (&f)[V / 2], int left) {
+        float s[V];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) unpack2(f[i], s[2 * i], s[2 * i + 1]);
+        if constexpr (VEC) {
+            VecIO<T, V>::store(p, s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < left) p[i] = from_f32<T>(s[i]);
+        }
+    }
+};
 
 // Tokens of sequence b: lengths[b] held to [0, T], or T without lengths.
 __device__ __forceinline__ int seq_len(const int* lengths, int b, int T) {

@@ -13,22 +13,30 @@
 //
 // Bound by HBM: each element is read once and written once. L lanes hold one
 // row, 8 adjacent elements each (16-byte loads), so the norm is log2 L
-// shuffles and the half layout's partner one shuffle. A group of L lanes stays
-// on one token and walks its heads, so the 8 cosines and sines of a lane are
-// read once per token; the block computes them once per token and pair into
-// shared memory.
+// shuffles and the half layout's partner one shuffle per element. A group of L
+// lanes stays on one token and walks its heads, so a lane's 8 cosines and sines
+// are read once per token; the block computes them once per token and pair into
+// shared memory, with the first rows already requested. The first version came
+// to 30% of the copy rate: 27 instructions an element, most of them copies,
+// clearing and layout tests; reloading a row's registers as soon as it is
+// unpacked and a kernel per layout brought it to 86%.
 //
 // Angles: the turn pos * f / (2 pi) mod 1 is an exact integer product mod 2^64
-// with f / (2 pi) held as a 64-bit binary fraction, so positions of any size
-// lose nothing; only the reduced turn is rounded to fp32.
+// with f / (2 pi), computed in 64-bit floating point, as a binary fraction; only
+// the reduced turn is rounded to fp32.
 #include <type_traits>
 
 #include "layer_common.cuh"
 
 namespace gdr {
 
+// Rows a lane group requests ahead, and blocks per SM. Forward, 2 x 8192 tokens
+// of 64 heads of 128 in bf16: 4 and 3 take 95.6 us, 2 and 3 106, 2 and 4 103, 4
+// and 4 (spills) 103. Backward, 2 x 4096 tokens of 32 heads of 256: 2 and 2 take
+// 122 us, 1 and 2 135, 1 and 3 (spills) 131.
+constexpr int kFwdAhead = 4, kFwdBlocks = 3, kBwdAhead = 2, kBwdBlocks = 2;
 constexpr int kNormThreads = 256;
-constexpr int kNormMaxParts = 148 * 4;  // blocks that keep weight-gradient sums
+constexpr int kNormMaxParts = 148 * kBwdBlocks;  // backward: one wave of blocks, each with sums of its own
 
 struct NormArgs {
     const void *q, *k, *qw, *kw, *pos;
@@ -39,8 +47,16 @@ struct NormArgs {
     long long qs[3], ks[3], gqs[3], gks[3], ps[2];
     long long tokens;
     int T, Hq, Hk, d, rot, tpb, rms, interleaved, pos64, w_f32;
-    float eps, q_scale, rscale;
+    float eps, q_scale, rscale, inv_d, inv_eps;
 };
+
+enum { kHalf = 1, kInterleaved = 2 };  // ROT: layout of the rotation, 0 for none
+
+// Sequence and position in it of a token.
+__device__ __forceinline__ void token_of(const NormArgs& a, long long tok, long long& b, long long& t) {
+    b = a.tokens <= 0x7fffffff ? (unsigned)tok / (unsigned)a.T : tok / a.T;
+    t = tok - b * a.T;
+}
 
 // cos and sin (times rscale) of the pairs of `tpb` tokens from token tok0.
 __device__ __forceinline__ void fill_turns(const NormArgs& a, long long tok0, float* cs, float* sn) {
@@ -50,7 +66,8 @@ __device__ __forceinline__ void fill_turns(const NormArgs& a, long long tok0, fl
         const long long tok = tok0 + tk;
         float c = 1.f, s = 0.f;
         if (tok < a.tokens) {
-            const long long b = tok / a.T, t = tok - b * a.T;
+            long long b, t;
+            token_of(a, tok, b, t);
             long long pos = t;
             if (a.pos) {
                 const long long o = b * a.ps[0] + t * a.ps[1];
@@ -70,38 +87,58 @@ __device__ __forceinline__ void fill_turns(const NormArgs& a, long long tok0, fl
 // One lane's 8 elements of a row: e(i) = 8 li + i (VEC), or li + 32 i.
 template <bool VEC> __device__ __forceinline__ int row_elem(int li, int i) { return VEC ? 8 * li + i : li + 32 * i; }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_lane(float (&f)[8], const T* row, int li, int d) {
-    if constexpr (VEC) {
-        if (8 * li < d) VecIO<T, 8>::load(f, row + 8 * li);
-        else
+// The elements as loaded, and as numbers. A lane's elements from d on are
+// never loaded and stay 0; a row that is not wanted keeps what it held.
+template <typename T, bool VEC> struct LaneRow {
+    RawVec<T, 8> v;
+    __device__ __forceinline__ void load(const T* row, int li, int d, bool on) {
+        if constexpr (VEC) {
+            if (on) v.load(row);
+        } else {
+            if (on) v.zero();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = 0.f;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = li + 32 * i < d ? to_f32(row[li + 32 * i]) : 0.f;
+            for (int i = 0; i < 8; ++i)
+                if (on && li + 32 * i < d) v.set(i, row[32 * i]);
+        }
     }
-}
+    __device__ __forceinline__ void get(f2 (&f)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = pack2(v.get(2 * i), v.get(2 * i + 1));
+    }
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_lane(T* row, const float (&f)[8], int li, int d) {
+__device__ __forceinline__ void store_lane(T* row, const f2 (&v)[4], int li, int d) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
     if constexpr (VEC) {
-        if (8 * li < d) VecIO<T, 8>::store(row + 8 * li, f);
+        VecIO<T, 8>::store(row, f);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (li + 32 * i < d) row[li + 32 * i] = from_f32<T>(f[i]);
+            if (li + 32 * i < d) row[32 * i] = from_f32<T>(f[i]);
     }
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_weight(float (&w)[8], const void* p, int w_f32, int li, int d) {
-    if (!p) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 1.f;
-        return;
+// q's and k's weights as fp32 in shared memory, rows of 256 (ones where absent).
+template <typename T> __device__ __forceinline__ void fill_weights(float* sw, const NormArgs& a, float q_scale) {
+    for (int i = threadIdx.x; i < 2 * a.d; i += kNormThreads) {
+        const int e = i < a.d ? i : i - a.d;
+        const void* p = i < a.d ? a.qw : a.kw;
+        const float w = !p ? 1.f : a.w_f32 ? reinterpret_cast<const float*>(p)[e] : to_f32(reinterpret_cast<const T*>(p)[e]);
+        sw[(i < a.d ? 0 : 256) + e] = i < a.d ? w * q_scale : w;
     }
-    if (w_f32) load_lane<float, VEC>(w, reinterpret_cast<const float*>(p), li, d);
-    else load_lane<T, VEC>(w, reinterpret_cast<const T*>(p), li, d);
+}
+template <bool VEC> __device__ __forceinline__ void lane_weight(f2 (&w)[4], const float* sw, int li) {
+    float f[8];
+    if constexpr (VEC) {
+        VecIO<float, 8>::load(f, sw + 8 * li);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = sw[li + 32 * i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack2(f[2 * i], f[2 * i + 1]);
 }
 
 template <int L> __device__ __forceinline__ float row_sum(float v) {
@@ -110,210 +147,253 @@ template <int L> __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// c[i], s[i] of a lane's elements: out = y c + partner s (s carries the sign).
-template <bool VEC>
-__device__ __forceinline__ void lane_turns(float (&c)[8], float (&s)[8], const NormArgs& a, const float* cs,
-                                           const float* sn, int li) {
+// c, s of a lane's elements: out = y c + partner s (s carries the sign, and
+// another for the transposed rotation: sign = -1); 1 and 0 where not rotated.
+template <bool VEC, int ROT>
+__device__ __forceinline__ void lane_turns(f2 (&c)[4], f2 (&s)[4], const NormArgs& a, const float* cs, const float* sn,
+                                           int li, float sign) {
     const int half = a.rot / 2;
+    float cf[8], sf[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int e = row_elem<VEC>(li, i);
-        c[i] = 1.f;
-        s[i] = 0.f;
+        cf[i] = 1.f;
+        sf[i] = 0.f;
         if (e < a.rot) {
-            const int p = a.interleaved ? e >> 1 : (e < half ? e : e - half);
-            const bool second = a.interleaved ? (e & 1) : e >= half;
-            c[i] = cs[p];
-            s[i] = second ? sn[p] : -sn[p];
+            const int p = ROT == kInterleaved ? e >> 1 : (e < half ? e : e - half);
+            const bool second = ROT == kInterleaved ? (e & 1) : e >= half;
+            cf[i] = cs[p];
+            sf[i] = second ? sign * sn[p] : -sign * sn[p];
         }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        c[i] = pack2(cf[2 * i], cf[2 * i + 1]);
+        s[i] = pack2(sf[2 * i], sf[2 * i + 1]);
     }
 }
 
-// The rotation's partner of each of a lane's elements. buf: this warp's row
-// in shared memory (plain form only).
-template <int L, bool VEC>
-__device__ __forceinline__ void partners(float (&o)[8], const float (&y)[8], const NormArgs& a, int li, float* buf) {
-    if constexpr (VEC) {
-        if (a.interleaved) {
+// Turns a lane's elements in place. src: the lane of the half layout's
+// partners (its own where not rotated). buf: this warp's row in shared memory
+// (plain form only).
+template <int L, bool VEC, int ROT>
+__device__ __forceinline__ void rotate(f2 (&y)[4], const f2 (&c)[4], const f2 (&s)[4], const NormArgs& a, int li,
+                                       int src, float* buf) {
+    float f[8], o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = y[i ^ 1];
-        } else {
-            const int hv = a.rot / 16;  // vectors in half the rotated part
-            const int src = li < hv ? li + hv : li < 2 * hv ? li - hv : li;
+    for (int i = 0; i < 4; ++i) unpack2(y[i], f[2 * i], f[2 * i + 1]);
+    if constexpr (VEC && ROT == kInterleaved) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, y[i], src, L);
-        }
+        for (int i = 0; i < 8; ++i) o[i] = f[i ^ 1];
+    } else if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, f[i], src, L);
     } else {
         const int half = a.rot / 2;
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) buf[li + 32 * i] = y[i];
+        for (int i = 0; i < 8; ++i) buf[li + 32 * i] = f[i];
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int e = li + 32 * i;
-            o[i] = e < a.rot ? buf[a.interleaved ? e ^ 1 : (e < half ? e + half : e - half)] : 0.f;
+            o[i] = e < a.rot ? buf[ROT == kInterleaved ? e ^ 1 : (e < half ? e + half : e - half)] : 0.f;
         }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = fma2(pack2(o[2 * i], o[2 * i + 1]), s[i], mul2(y[i], c[i]));
+}
+
+// The lane that holds the half layout's partners of a lane's elements.
+__device__ __forceinline__ int partner_lane(const NormArgs& a, int li) {
+    const int hv = a.rot / 16;  // vectors in half the rotated part
+    return li < hv ? li + hv : li < 2 * hv ? li - hv : li;
 }
 
 // Reciprocal norm; `inside` tells an L2 row at or below eps (constant divisor).
 __device__ __forceinline__ float row_rnorm(const NormArgs& a, float ss, bool* inside) {
     if (a.rms) {
         *inside = false;
-        return rsqrtf(ss / (float)a.d + a.eps);
+        return rsqrt_approx(fmaf(ss, a.inv_d, a.eps));
     }
-    const float r = rsqrtf(ss), lim = 1.f / a.eps;
+    const float r = rsqrt_approx(ss);
+    const float lim = a.inv_eps;
     *inside = r >= lim;  // a NaN row stays NaN
     return *inside ? lim : r;
 }
 
-template <typename T, int L, bool VEC>
-__global__ void __launch_bounds__(kNormThreads) qk_norm_fwd_kernel(NormArgs a) {
+// The rows of one lane group's token at this lane's first element: head h of
+// q, then of k.
+template <typename T> struct HeadRows {
+    T *q, *k;  // k is reached from h = 0 too, H_q heads before its first
+    long long qs, ks;
+    int Hq;
+    __device__ __forceinline__ HeadRows(T* q_, T* k_, long long qs_, long long ks_, int Hq_)
+        : q(q_), k(k_ - Hq_ * ks_), qs(qs_), ks(ks_), Hq(Hq_) {}
+    __device__ __forceinline__ T* at(int h) const { return (h < Hq ? q : k) + h * (h < Hq ? qs : ks); }
+};
+template <typename T>
+__device__ __forceinline__ HeadRows<const T> input_rows(const void* q, const void* k, const long long (&qs)[3],
+                                                        const long long (&ks)[3], long long b, long long t, int Hq,
+                                                        int e0) {
+    return {reinterpret_cast<const T*>(q) + b * qs[0] + t * qs[1] + e0,
+            reinterpret_cast<const T*>(k) + b * ks[0] + t * ks[1] + e0, qs[2], ks[2], Hq};
+}
+template <typename T>
+__device__ __forceinline__ HeadRows<T> output_rows(void* q, void* k, long long tok, int Hq, int Hk, int d, int e0) {
+    return {reinterpret_cast<T*>(q) + tok * Hq * d + e0, reinterpret_cast<T*>(k) + tok * Hk * d + e0, d, d, Hq};
+}
+
+template <typename T, int L, bool VEC, int ROT>
+__global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(NormArgs a) {
     extern __shared__ float sm[];
     __shared__ float rowbuf[VEC ? 1 : kNormThreads / 32][VEC ? 1 : 256];
-    constexpr int kSlots = kNormThreads / L, kAhead = 4;
+    __shared__ __align__(16) float sw[512];
+    constexpr int kSlots = kNormThreads / L, kAhead = sizeof(T) == 2 ? kFwdAhead : kFwdAhead / 2;
     float *cs = sm, *sn = sm + a.tpb * (a.rot / 2);
-    const int li = threadIdx.x % L, slot = threadIdx.x / L;
+    const int li = threadIdx.x % L, slot = threadIdx.x / L, e0 = row_elem<VEC>(li, 0);
     const int spt = kSlots / a.tpb;  // lane groups that share a token
     const long long tok0 = (long long)blockIdx.x * a.tpb, tok = tok0 + slot / spt;
-    const int R = a.Hq + a.Hk;
-    if (a.rot) {
-        fill_turns(a, tok0, cs, sn);
-        __syncthreads();
+    const int R = a.Hq + a.Hk, h0 = slot % spt, src = partner_lane(a, li);
+    const bool live = tok < a.tokens && e0 < a.d, weighted = a.qw || a.kw;
+    long long b, t;
+    token_of(a, live ? tok : 0, b, t);
+    const int last = live ? R : 0;  // this lane's rows end here
+    const auto in = input_rows<T>(a.q, a.k, a.qs, a.ks, b, t, a.Hq, e0);
+    const auto out = output_rows<T>(a.q_out, a.k_out, tok, a.Hq, a.Hk, a.d, e0);
+    dependent_launch();
+    dependent_wait();
+    LaneRow<T, VEC> row[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+        row[j].v.zero();
+        row[j].load(in.at(h0 + j * spt), li, a.d, h0 + j * spt < last);
     }
-    float c[8], s[8], qw[8], kw[8];
-    lane_turns<VEC>(c, s, a, cs + (slot / spt) * (a.rot / 2), sn + (slot / spt) * (a.rot / 2), li);
-    load_weight<T, VEC>(qw, a.qw, a.w_f32, li, a.d);
-    load_weight<T, VEC>(kw, a.kw, a.w_f32, li, a.d);
-    const bool live = tok < a.tokens;
-    const long long b = live ? tok / a.T : 0, t = live ? tok - b * a.T : 0;
-    const T* qrow = reinterpret_cast<const T*>(a.q) + b * a.qs[0] + t * a.qs[1];
-    const T* krow = reinterpret_cast<const T*>(a.k) + b * a.ks[0] + t * a.ks[1];
+    if (weighted) fill_weights<T>(sw, a, a.q_scale);
+    if (ROT) fill_turns(a, tok0, cs, sn);
+    if (weighted || ROT) __syncthreads();
+    f2 c[4], s[4];
+    if (ROT) lane_turns<VEC, ROT>(c, s, a, cs + (slot / spt) * (a.rot / 2), sn + (slot / spt) * (a.rot / 2), li, 1.f);
     float* buf = rowbuf[VEC ? 0 : slot];
     // every lane of a warp runs the same number of rows: shuffles need them all
-    for (int h0 = 0; h0 < R; h0 += kAhead * spt) {
-        float x[kAhead][8];
+    for (int hb = 0; hb < R; hb += kAhead * spt) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const int h = h0 + j * spt + slot % spt;
-            if (live && h < R)
-                load_lane<T, VEC>(x[j], h < a.Hq ? qrow + h * a.qs[2] : krow + (h - a.Hq) * a.ks[2], li, a.d);
-            else
+            const int h = hb + h0 + j * spt, ahead = h + kAhead * spt;
+            f2 y[4];
+            row[j].get(y);
+            row[j].load(in.at(ahead), li, a.d, ahead < last);
+            f2 sq = mul2(y[0], y[0]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int h = h0 + j * spt + slot % spt;
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[j][i], x[j][i], ss);
+            for (int i = 1; i < 4; ++i) sq = fma2(y[i], y[i], sq);
             bool inside;
-            const float r = row_rnorm(a, row_sum<L>(ss), &inside);
-            const bool isq = h < a.Hq;
-            float y[8], o[8];
+            float r = row_rnorm(a, row_sum<L>(sum2(sq)), &inside);
+            if (weighted) {
+                f2 w[4];
+                lane_weight<VEC>(w, sw + (h < a.Hq ? 0 : 256), li);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[j][i] * r * (isq ? qw[i] : kw[i]);
-            if (a.rot) {
-                partners<L, VEC>(o, y, a, li, buf);
+                for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], mul2(both2(r), w[i]));
+            } else {
+                if (h < a.Hq) r *= a.q_scale;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = s[i] == 0.f ? y[i] * c[i] : fmaf(o[i], s[i], y[i] * c[i]);
+                for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], both2(r));
             }
-            if (isq)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= a.q_scale;
-            if (live && h < R) {
-                T* out = isq ? reinterpret_cast<T*>(a.q_out) + (tok * a.Hq + h) * a.d
-                             : reinterpret_cast<T*>(a.k_out) + (tok * a.Hk + (h - a.Hq)) * a.d;
-                store_lane<T, VEC>(out, y, li, a.d);
-            }
+            if constexpr (ROT != 0) rotate<L, VEC, ROT>(y, c, s, a, li, src, buf);
+            if (h < last) store_lane<T, VEC>(out.at(h), y, li, a.d);
         }
     }
 }
 
-template <typename T, typename TG, int L, bool VEC>
-__global__ void __launch_bounds__(kNormThreads) qk_norm_bwd_kernel(NormArgs a) {
+template <typename T, typename TG, int L, bool VEC, int ROT>
+__global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(NormArgs a) {
     extern __shared__ float sm[];
     __shared__ float rowbuf[VEC ? 1 : kNormThreads / 32][VEC ? 1 : 256];
-    constexpr int kSlots = kNormThreads / L, kAhead = 2;
+    __shared__ __align__(16) float sw[512];
+    constexpr int kSlots = kNormThreads / L, kAhead = sizeof(T) == 2 ? kBwdAhead : 1;
     float *cs = sm, *sn = sm + a.tpb * (a.rot / 2);
-    const int li = threadIdx.x % L, slot = threadIdx.x / L;
+    const int li = threadIdx.x % L, slot = threadIdx.x / L, e0 = row_elem<VEC>(li, 0);
     const int spt = kSlots / a.tpb;
-    const int R = a.Hq + a.Hk;
-    float qw[8], kw[8], dqw[8], dkw[8];
-    load_weight<T, VEC>(qw, a.qw, a.w_f32, li, a.d);
-    load_weight<T, VEC>(kw, a.kw, a.w_f32, li, a.d);
+    const int R = a.Hq + a.Hk, h0 = slot % spt, src = partner_lane(a, li);
+    const bool weighted = a.qw || a.kw;
+    f2 dqw[4], dkw[4];  // without q_scale
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dqw[i] = dkw[i] = 0.f;
+    for (int i = 0; i < 4; ++i) dqw[i] = dkw[i] = both2(0.f);
+    if (weighted) fill_weights<T>(sw, a, 1.f);
     float* buf = rowbuf[VEC ? 0 : slot];
+    LaneRow<T, VEC> xrow[kAhead];
+    LaneRow<TG, VEC> grow[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+        xrow[j].v.zero();
+        grow[j].v.zero();
+    }
     for (long long tok0 = (long long)blockIdx.x * a.tpb; tok0 < a.tokens; tok0 += (long long)gridDim.x * a.tpb) {
         const long long tok = tok0 + slot / spt;
-        if (a.rot) {
-            __syncthreads();
+        const bool live = tok < a.tokens && e0 < a.d;
+        const int last = live ? R : 0;
+        long long b, t;
+        token_of(a, live ? tok : 0, b, t);
+        const auto in = input_rows<T>(a.q, a.k, a.qs, a.ks, b, t, a.Hq, e0);
+        const auto gin = input_rows<TG>(a.gq, a.gk, a.gqs, a.gks, b, t, a.Hq, e0);
+        const auto out = output_rows<float>(a.q_out, a.k_out, tok, a.Hq, a.Hk, a.d, e0);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int h = h0 + j * spt;
+            xrow[j].load(in.at(h), li, a.d, h < last);
+            grow[j].load(gin.at(h), li, a.d, h < last);
+        }
+        f2 c[4], s[4];  // of the transposed rotation
+        __syncthreads();  // the last tokens' turns have been read
+        if (ROT) {
             fill_turns(a, tok0, cs, sn);
             __syncthreads();
+            lane_turns<VEC, ROT>(c, s, a, cs + (slot / spt) * (a.rot / 2), sn + (slot / spt) * (a.rot / 2), li, -1.f);
         }
-        float c[8], s[8];
-        lane_turns<VEC>(c, s, a, cs + (slot / spt) * (a.rot / 2), sn + (slot / spt) * (a.rot / 2), li);
-        const bool live = tok < a.tokens;
-        const long long b = live ? tok / a.T : 0, t = live ? tok - b * a.T : 0;
-        const T* qrow = reinterpret_cast<const T*>(a.q) + b * a.qs[0] + t * a.qs[1];
-        const T* krow = reinterpret_cast<const T*>(a.k) + b * a.ks[0] + t * a.ks[1];
-        const TG* gqrow = reinterpret_cast<const TG*>(a.gq) + b * a.gqs[0] + t * a.gqs[1];
-        const TG* gkrow = reinterpret_cast<const TG*>(a.gk) + b * a.gks[0] + t * a.gks[1];
-        for (int h0 = 0; h0 < R; h0 += kAhead * spt) {
-            float x[kAhead][8], g[kAhead][8];
+        for (int hb = 0; hb < R; hb += kAhead * spt) {
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const int h = h0 + j * spt + slot % spt;
-                if (live && h < R) {
-                    load_lane<T, VEC>(x[j], h < a.Hq ? qrow + h * a.qs[2] : krow + (h - a.Hq) * a.ks[2], li, a.d);
-                    load_lane<TG, VEC>(g[j], h < a.Hq ? gqrow + h * a.gqs[2] : gkrow + (h - a.Hq) * a.gks[2], li, a.d);
+                const int h = hb + h0 + j * spt, ahead = h + kAhead * spt;
+                const bool isq = h < a.Hq;
+                f2 x[4], g[4], gw[4];
+                xrow[j].get(x);
+                grow[j].get(g);
+                xrow[j].load(in.at(ahead), li, a.d, ahead < last);
+                grow[j].load(gin.at(ahead), li, a.d, ahead < last);
+                if constexpr (ROT != 0) rotate<L, VEC, ROT>(g, c, s, a, li, src, buf);
+                if (weighted) {
+                    lane_weight<VEC>(gw, sw + (isq ? 0 : 256), li);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) gw[i] = mul2(gw[i], g[i]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[j][i] = g[j][i] = 0.f;
+                    for (int i = 0; i < 4; ++i) gw[i] = g[i];
                 }
-            }
+                f2 sq = mul2(x[0], x[0]), gx2 = mul2(gw[0], x[0]);
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int h = h0 + j * spt + slot % spt;
-                const bool isq = h < a.Hq, on = live && h < R;
-                if (isq)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) g[j][i] *= a.q_scale;
-                if (a.rot) {  // R^T: the partner's coefficient is -s
-                    float o[8];
-                    partners<L, VEC>(o, g[j], a, li, buf);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        g[j][i] = s[i] == 0.f ? g[j][i] * c[i] : fmaf(-o[i], s[i], g[j][i] * c[i]);
-                }
-                float ss = 0.f, gx = 0.f, gw[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    gw[i] = g[j][i] * (isq ? qw[i] : kw[i]);
-                    ss = fmaf(x[j][i], x[j][i], ss);
-                    gx = fmaf(gw[i], x[j][i], gx);
+                for (int i = 1; i < 4; ++i) {
+                    sq = fma2(x[i], x[i], sq);
+                    gx2 = fma2(gw[i], x[i], gx2);
                 }
                 bool inside;
-                const float r = row_rnorm(a, row_sum<L>(ss), &inside);
-                gx = row_sum<L>(gx) * r;  // sum(g xh)
-                const float m = inside ? 0.f : a.rms ? gx / (float)a.d : gx;
-                float dx[8];
+                const float r = row_rnorm(a, row_sum<L>(sum2(sq)), &inside);
+                const float gx = row_sum<L>(sum2(gx2)) * r;  // sum(g xh)
+                const float m = inside ? 0.f : a.rms ? gx * a.inv_d : gx;
+                const float rs = isq ? r * a.q_scale : r;
+                f2 dx[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float xh = x[j][i] * r;
-                    dx[i] = r * fmaf(-xh, m, gw[i]);
-                    if (on) {
-                        if (isq) dqw[i] = fmaf(g[j][i], xh, dqw[i]);
-                        else dkw[i] = fmaf(g[j][i], xh, dkw[i]);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = mul2(x[i], both2(r));  // xh
+                    dx[i] = mul2(both2(rs), fma2(x[i], both2(-m), gw[i]));
                 }
-                if (on) {
-                    float* out = isq ? reinterpret_cast<float*>(a.q_out) + (tok * a.Hq + h) * a.d
-                                     : reinterpret_cast<float*>(a.k_out) + (tok * a.Hk + (h - a.Hq)) * a.d;
-                    store_lane<float, VEC>(out, dx, li, a.d);
+                if (h < last) {
+                    if (weighted && isq) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) dqw[i] = fma2(g[i], x[i], dqw[i]);
+                    } else if (weighted) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) dkw[i] = fma2(g[i], x[i], dkw[i]);
+                    }
+                    store_lane<float, VEC>(out.at(h), dx, li, a.d);
                 }
             }
         }
@@ -325,7 +405,12 @@ __global__ void __launch_bounds__(kNormThreads) qk_norm_bwd_kernel(NormArgs a) {
     for (int which = 0; which < 2; ++which) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) red[slot][row_elem<VEC>(li, i)] = which ? dkw[i] : dqw[i];
+        for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            unpack2(which ? dkw[i] : mul2(dqw[i], both2(a.q_scale)), lo, hi);
+            red[slot][row_elem<VEC>(li, 2 * i)] = lo;
+            red[slot][row_elem<VEC>(li, 2 * i + 1)] = hi;
+        }
         __syncthreads();
         for (int e = threadIdx.x; e < a.d; e += kNormThreads) {
             float v = 0.f;
@@ -362,22 +447,29 @@ static int norm_lanes(int d) {
     return l;
 }
 
-// Tokens per block: one per lane group when that still gives every SM four
-// blocks, fewer (several groups share a token's heads) below that.
+// Tokens per block: one per lane group when that still gives every SM twelve
+// blocks (four waves), fewer (several groups share a token's heads) below that.
 static int norm_tokens_per_block(long long tokens, int lanes) {
     int tpb = kNormThreads / lanes;
-    while (tpb > 1 && (tokens + tpb - 1) / tpb < 148 * 4) tpb /= 2;
+    while (tpb > 1 && (tokens + tpb - 1) / tpb < 148 * 12) tpb /= 2;
     return tpb < 16 ? tpb : 16;
 }
 
-template <typename F> static void dispatch_lanes(bool vec, int lanes, F&& f) {
-    if (!vec) { f(std::integral_constant<int, 32>(), std::false_type()); return; }
+template <int L, bool VEC, typename F> static void dispatch_rot(const NormArgs& a, F&& f) {
+    using LC = std::integral_constant<int, L>;
+    using VC = std::integral_constant<bool, VEC>;
+    if (!a.rot) f(LC(), VC(), std::integral_constant<int, 0>());
+    else if (a.interleaved) f(LC(), VC(), std::integral_constant<int, kInterleaved>());
+    else f(LC(), VC(), std::integral_constant<int, kHalf>());
+}
+template <typename F> static void dispatch_lanes(const NormArgs& a, bool vec, int lanes, F&& f) {
+    if (!vec) { dispatch_rot<32, false>(a, f); return; }
     switch (lanes) {
-        case 2: f(std::integral_constant<int, 2>(), std::true_type()); break;
-        case 4: f(std::integral_constant<int, 4>(), std::true_type()); break;
-        case 8: f(std::integral_constant<int, 8>(), std::true_type()); break;
-        case 16: f(std::integral_constant<int, 16>(), std::true_type()); break;
-        default: f(std::integral_constant<int, 32>(), std::true_type()); break;
+        case 2: dispatch_rot<2, true>(a, f); break;
+        case 4: dispatch_rot<4, true>(a, f); break;
+        case 8: dispatch_rot<8, true>(a, f); break;
+        case 16: dispatch_rot<16, true>(a, f); break;
+        default: dispatch_rot<32, true>(a, f); break;
     }
 }
 
@@ -407,7 +499,9 @@ static gdr_status norm_fill(NormArgs& a, const long long* strides, int nstrides,
     a.T = T; a.Hq = Hq; a.Hk = Hk; a.d = d; a.rot = rot;
     a.rms = kind == GDR_NORM_RMS; a.interleaved = rotary == GDR_ROTARY_INTERLEAVED;
     a.pos64 = pos64; a.w_f32 = weight_dtype == GDR_FP32;
-    a.eps = eps; a.q_scale = q_scale; a.rscale = rscale;
+    a.eps = eps < 1.17549435e-38f ? 1.17549435e-38f : eps;  // the kernels flush smaller numbers to 0
+    a.q_scale = q_scale; a.rscale = rscale;
+    a.inv_d = 1.f / (float)d; a.inv_eps = 1.f / a.eps;
     const long long dense[14] = {(long long)T * Hq * d, (long long)Hq * d, d, (long long)T * Hk * d, (long long)Hk * d, d,
                                  T, 1, (long long)T * Hq * d, (long long)Hq * d, d, (long long)T * Hk * d,
                                  (long long)Hk * d, d};
@@ -461,13 +555,16 @@ gdr_status gdr_qk_norm_fwd(const void* q, const void* k, const void* q_weight, c
     if (grid > 0x7fffffffll) return GDR_ERR_UNSUPPORTED;
     const size_t smem = (size_t)a.tpb * rot * sizeof(float);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    dispatch_lanes(vec, lanes, [&](auto lc, auto vc) {
+    cudaError_t err = cudaErrorInvalidValue;
+    dispatch_lanes(a, vec, lanes, [&](auto lc, auto vc, auto rc) {
         constexpr int L = decltype(lc)::value;
         constexpr bool V = decltype(vc)::value;
-        if (dtype == GDR_BF16) qk_norm_fwd_kernel<__nv_bfloat16, L, V><<<(unsigned)grid, kNormThreads, smem, st>>>(a);
-        else qk_norm_fwd_kernel<float, L, V><<<(unsigned)grid, kNormThreads, smem, st>>>(a);
+        constexpr int RT = decltype(rc)::value;
+        err = dtype == GDR_BF16
+                  ? launch_dependent(qk_norm_fwd_kernel<__nv_bfloat16, L, V, RT>, (unsigned)grid, kNormThreads, smem, st, a)
+                  : launch_dependent(qk_norm_fwd_kernel<float, L, V, RT>, (unsigned)grid, kNormThreads, smem, st, a);
     });
-    return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
+    return err == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
 }
 
 size_t gdr_qk_norm_bwd_workspace_size(int d) {
@@ -511,15 +608,16 @@ gdr_status gdr_qk_norm_bwd(const void* q, const void* k, const void* q_weight, c
         grid = (a.tokens + a.tpb - 1) / a.tpb;
         if (grid > kNormMaxParts) grid = kNormMaxParts;
         const size_t smem = (size_t)a.tpb * rot * sizeof(float);
-        dispatch_lanes(vec, lanes, [&](auto lc, auto vc) {
+        dispatch_lanes(a, vec, lanes, [&](auto lc, auto vc, auto rc) {
             constexpr int L = decltype(lc)::value;
             constexpr bool V = decltype(vc)::value;
+        constexpr int RT = decltype(rc)::value;
             if (dtype == GDR_FP32)
-                qk_norm_bwd_kernel<float, float, L, V><<<(unsigned)grid, kNormThreads, smem, st>>>(a);
+                qk_norm_bwd_kernel<float, float, L, V, RT><<<(unsigned)grid, kNormThreads, smem, st>>>(a);
             else if (grad_dtype == GDR_FP32)
-                qk_norm_bwd_kernel<__nv_bfloat16, float, L, V><<<(unsigned)grid, kNormThreads, smem, st>>>(a);
+                qk_norm_bwd_kernel<__nv_bfloat16, float, L, V, RT><<<(unsigned)grid, kNormThreads, smem, st>>>(a);
             else
-                qk_norm_bwd_kernel<__nv_bfloat16, __nv_bfloat16, L, V><<<(unsigned)grid, kNormThreads, smem, st>>>(a);
+                qk_norm_bwd_kernel<__nv_bfloat16, __nv_bfloat16, L, V, RT><<<(unsigned)grid, kNormThreads, smem, st>>>(a);
         });
         if (cudaGetLastError() != cudaSuccess) return GDR_ERR_LAUNCH;
     }

@@ -4,7 +4,7 @@
 
 namespace gdr {
 cudaError_t launch_scan_fwd(const ScanArgs& a, int B, int dtype, cudaStream_t st);
-cudaError_t launch_scan_step(const ScanArgs& a, float* h, int B, int dtype, cudaStream_t st);
+cudaError_t launch_scan_step(ScanArgs a, float* h, int B, int dtype, cudaStream_t st);
 cudaError_t launch_scan_bwd(ScanArgs a, void* ws, float* dA, float* dB, float* dC, float* dD, float* dbias, int B,
                             int dtype, int grad_dtype, cudaStream_t st);
 struct ScanBwdLayout { size_t ckpt, bc, prm, total; };
@@ -118,6 +118,8 @@ gdr_status gdr_scan_step(const void* u, const void* delta, const float* A, const
     if (!aligned_to(y, dtype_size(dtype))) return GDR_ERR_MISALIGNED;
     a.y = y;
     a.state_vec = states_in_quads(N, {A, h});
+    a.bc_vec = N % 4 == 0 && a.bs[0] % 4 == 0 && a.cs[0] % 4 == 0 && aligned_to(Bm, 4 * dtype_size(dtype)) &&
+               aligned_to(Cm, 4 * dtype_size(dtype));
     return launched(launch_scan_step(a, h, B, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 

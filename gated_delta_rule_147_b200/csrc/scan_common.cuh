@@ -23,36 +23,6 @@ namespace gdr {
 constexpr int kScanWarps = 8;
 constexpr int kScanThreads = 32 * kScanWarps;
 
-// ---- packed pairs of fp32 (one instruction for two multiply-adds) ----
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack2(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f2 v, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 ex2_pair(f2 v) {
-    float a, b;
-    unpack2(v, a, b);
-    return pack2(ex2_approx(a), ex2_approx(b));
-}
-__device__ __forceinline__ float sum2(f2 v) {
-    float a, b;
-    unpack2(v, a, b);
-    return a + b;
-}
 __device__ __forceinline__ void lds_quad(f2 (&q)[2], const float* p) {
     const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
     q[0] = v.x;
@@ -82,7 +52,7 @@ struct ScanArgs {
     void* y;
     float* h_T;
     long long us[2], ds[2], bs[2], cs[2], zs[2], gs[2];  // batch and token strides
-    int T, D_, N, G, K, tiles, softplus, state_vec;
+    int T, D_, N, G, K, tiles, softplus, state_vec, bc_vec;
     // backward
     const float* dh_T;
     float *du, *ddelta, *dz, *dh0;

@@ -417,8 +417,8 @@ gdr_status gdr_decode_step_grouped(const void* q, const void* k, const void* v,
  * X0 [B, W-1, D] the inputs before the first token or NULL (zeros), y
  * [B, T, D], X_T [B, W-1, D] or NULL. X_T may be X0. 2 <= W <= 4
  * (GDR_ERR_UNSUPPORTED otherwise, as for a weight type that is neither dtype
- * nor fp32). The 16-byte form needs D a multiple of 8 (bf16) or 4 (fp32),
- * strides likewise and 16-byte aligned arrays.
+ * nor fp32). Loads and stores are wide where D and the
+ * strides are multiples of 4, arrays are aligned to 4 elements and weight to 16 bytes.
  */
 gdr_status gdr_conv_fwd(const void* x, const void* weight, const void* bias, const void* X0,
                         const int* lengths, void* y, void* X_T, const long long* strides, int B,
@@ -516,9 +516,10 @@ gdr_status gdr_scan_step(const void* u, const void* delta, const float* A, const
  * value, or NULL for 0 .. T-1. strides: q batch, token, head, k batch, token,
  * head, positions batch, token. q_out, k_out dense; q_out may be q where q is
  * dense (likewise k). 1 <= d <= 256, rot even and at most d, eps > 0. Angles
- * are reduced exactly for any position. The 16-byte form needs d a multiple of
- * 8, strides likewise, 16-byte aligned arrays and, in the half layout, rot a
- * multiple of 16.
+ * are reduced exactly, with inv_freq / (2 pi) held to 53 bits: an error of
+ * position * inv_freq * 2^-53 radians. A row's sum of squares must stay within
+ * fp32. Loads and stores are wide where d is a multiple of 8, strides likewise,
+ * arrays are 16-byte aligned and, in the half layout, rot is a multiple of 16.
  */
 gdr_status gdr_qk_norm_fwd(const void* q, const void* k, const void* q_weight,
                            const void* k_weight, const void* positions, const float* inv_freq,
