@@ -25,7 +25,7 @@ EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_grouped", "gdr_chunk_fwd_workspace_si
            "gdr_chunk_bwd_workspace_size", "gdr_chunk_bwd_grouped",
            "gdr_chunk_bwd_grouped_workspace_size", "gdr_decode_step",
            "gdr_decode_step_grouped", "gdr_conv_fwd", "gdr_conv_bwd",
-           "gdr_conv_bwd_workspace_size", "gdr_conv_step", "gdr_scan_fwd", "gdr_scan_bwd",
+           "gdr_conv_bwd_workspace_size", "gdr_conv_step", "gdr_scan_fwd", "gdr_scan_fwd_workspace_size", "gdr_scan_bwd",
            "gdr_scan_bwd_workspace_size", "gdr_scan_step", "gdr_qk_norm_fwd", "gdr_qk_norm_bwd",
            "gdr_qk_norm_bwd_workspace_size", "gdr_selftest_bounded_wait", "gdr_status_string",
            "gdr_version")
@@ -83,7 +83,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         for fn, args in (("gdr_conv_fwd", [vp] * 8 + [ip] * 7 + [vp]),
                          ("gdr_conv_bwd", [vp] * 12 + [sz, vp] + [ip] * 8 + [vp]),
                          ("gdr_conv_step", [vp] * 6 + [ip] * 6 + [vp]),
-                         ("gdr_scan_fwd", [vp] * 13 + [ip] * 7 + [vp]),
+                         ("gdr_scan_fwd", [vp] * 13 + [sz, vp] + [ip] * 7 + [vp]),
                          ("gdr_scan_bwd", [vp] * 22 + [sz, vp] + [ip] * 8 + [vp]),
                          ("gdr_scan_step", [vp] * 11 + [ip] * 6 + [vp]),
                          ("gdr_qk_norm_fwd", [vp] * 9 + [ip] * 8 + [fp] * 3 + [ip] * 3 + [vp]),
@@ -231,7 +231,7 @@ def _layer_call(name, argc):
 gdr_conv_fwd = _layer_call("gdr_conv_fwd", 15)
 gdr_conv_bwd = _layer_call("gdr_conv_bwd", 22)
 gdr_conv_step = _layer_call("gdr_conv_step", 12)
-gdr_scan_fwd = _layer_call("gdr_scan_fwd", 20)
+gdr_scan_fwd = _layer_call("gdr_scan_fwd", 22)
 gdr_scan_bwd = _layer_call("gdr_scan_bwd", 32)
 gdr_scan_step = _layer_call("gdr_scan_step", 17)
 gdr_qk_norm_fwd = _layer_call("gdr_qk_norm_fwd", 23)
@@ -240,6 +240,10 @@ gdr_qk_norm_bwd = _layer_call("gdr_qk_norm_bwd", 30)
 
 def gdr_conv_bwd_workspace_size(B, T, D, W) -> int:
     return int(load().gdr_conv_bwd_workspace_size(B, T, D, W))
+
+
+def gdr_scan_fwd_workspace_size(B, T, D, N, G) -> int:
+    return int(load().gdr_scan_fwd_workspace_size(B, T, D, N, G))
 
 
 def gdr_scan_bwd_workspace_size(B, T, D, N, G) -> int:

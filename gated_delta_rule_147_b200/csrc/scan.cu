@@ -1,195 +1,195 @@
 // Selective state-space scan: forward over whole sequences (also the backward
 // pass's state checkpoints) and one token per sequence.
 //
-// The forward's floor is its exponentials: N per token and channel at 16 per
-// clock and SM, against 6 to 8 bytes of HBM traffic. One pass computes each
-// exponential once. Per pair of states and token, in packed fp32:
-// dt A, exp2 (twice), dt u B, h, C h, and, so that a segment can start before
-// its incoming state is known, the running decay p and C p. When the state
-// arrives, y += (C p) h_in is one multiply-add, and the outgoing state
-// p h_in + h goes on to the next warp before that.
+// The forward's floor is its exponentials: N per token and channel, and two with
+// a reciprocal for softplus and gate, at 16 per clock and SM, against 6 to 8
+// bytes of HBM traffic. Per pair of states and token a walker does dt A, exp2
+// (twice), dt u B, h and C h in packed fp32.
+//
+// Where the channels alone leave SMs empty the tokens are split into chunks:
+// one launch finds each chunk's map of its start state (decay and end from
+// zero), and the second, whose blocks fold the maps before theirs, does the
+// rest. That computes the exponentials twice, so it takes three chunks at least.
 #include <type_traits>
 
 #include "scan_common.cuh"
 
 namespace gdr {
 
-template <typename T, typename Gm, bool CKPT>
-__global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(ScanArgs a) {
-    constexpr int CH = Gm::CH, L = Gm::L, CPW = Gm::CPW, NP = Gm::NP;
+enum { kScanOut = 0, kScanEnds = 1, kScanCkpt = 2 };  // y; chunk maps; states every Seg tokens
+
+template <typename T, typename Gm, int MODE>
+__global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a) {
+    constexpr int CH = Gm::CH, LT = Gm::LT, CB = Gm::CB, CL = Gm::CL, NP = Gm::NP;
+    constexpr int kIn = 4 * LT * CB + 2 * LT * NP, kOut = LT * CB * Gm::NQ;  // floats of a step: (dt, dt u), B, C; sums
     extern __shared__ __align__(16) float sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nl = lane % Gm::NS, cl = lane / Gm::NS;
-    constexpr int kWarpFloats = 3 * L * CPW + 2 * L * NP;
-    float* sdt = sm + warp * kWarpFloats;
-    float* sdtu = sdt + L * CPW;
-    float* sy = sdtu + L * CPW;
-    float* sB = sy + L * CPW;
-    float* sC = sB + L * NP;
-    float* carry = sm + kScanWarps * kWarpFloats;  // [warp][CH][32] quads: the state a warp starts from
-    const ScanTile tl(a, CPW);
-    const T* u = reinterpret_cast<const T*>(a.u) + tl.b * a.us[0] + tl.c0;
-    const T* dl = reinterpret_cast<const T*>(a.delta) + tl.b * a.ds[0] + tl.c0;
-    const T* z = a.z ? reinterpret_cast<const T*>(a.z) + tl.b * a.zs[0] + tl.c0 : nullptr;
-    const T* Bm = reinterpret_cast<const T*>(a.Bm) + tl.b * a.bs[0] + tl.g * a.N;
-    const T* Cm = reinterpret_cast<const T*>(a.Cm) + tl.b * a.cs[0] + tl.g * a.N;
-    T* y = reinterpret_cast<T*>(a.y) + (size_t)tl.b * a.T * a.D_ + tl.c0;
-    const size_t sbase = (size_t)tl.b * a.D_ * a.N;
-    const int nseg = (tl.n + L - 1) / L;
+    const ScanTile tl(a, CB);
+    if (MODE == kScanEnds && tl.part + 1 == a.chunks) return;  // no chunk after it
+    const int steps = (tl.n - tl.t0 + LT - 1) / LT;
+    float* const out = sm + 2 * kIn;
 
-    f2 A[CH][2];
-    load_states<Gm>(A, a.A, tl, a.N, a.state_vec, cl, nl, kLog2e, true);
-    // a lane's staged elements keep their channel from segment to segment
-    float bias[Gm::SE], skip[Gm::SE];
+    if (warp < kWalkers) {
+        const int nl = lane % Gm::NS, cl = lane / Gm::NS, ch0 = warp * Gm::CPW + cl * CH;
+        f2 A[CH][2], h[CH][2];
+        load_states<Gm>(A, a.A, tl, a.N, a.state_vec, ch0, nl, kLog2e, true);
+        load_given<Gm>(h, MODE == kScanEnds ? nullptr : a.h0, a, tl, ch0, nl);
+        if (MODE != kScanEnds) fold_chunks<Gm>(h, a.ends, a, tl, warp, lane, 0, tl.part, 1);
+        f2 total[CH];  // sum of dt
+        if (MODE == kScanEnds)
 #pragma unroll
-    for (int i = 0; i < Gm::SE; ++i) {
-        const int ch = (32 * i + lane) % CPW;
-        bias[i] = a.bias && ch < tl.kleft ? a.bias[tl.c0 + ch] : 0.f;
-        skip[i] = !CKPT && a.D && ch < tl.kleft ? a.D[tl.c0 + ch] : 0.f;
-    }
-    T ru[Gm::SE], rd[Gm::SE], rz[Gm::SE], rB[Gm::BE], rC[Gm::BE];
-    auto fetch = [&](int seg) {
-        fetch_rows<T, Gm>(ru, u, a.us[1], seg * L, tl, lane);
-        fetch_rows<T, Gm>(rd, dl, a.ds[1], seg * L, tl, lane);
-        fetch_vecs<T, Gm>(rB, Bm, a.bs[1], seg * L, tl, a.N, lane);
-        if constexpr (!CKPT) {
-            if (z) fetch_rows<T, Gm>(rz, z, a.zs[1], seg * L, tl, lane);
-            fetch_vecs<T, Gm>(rC, Cm, a.cs[1], seg * L, tl, a.N, lane);
-        }
-    };
-    if (warp < nseg) fetch(warp);
-    for (int seg = warp; seg < nseg; seg += kScanWarps) {
-        float du[Gm::SE], gate[Gm::SE];  // D u and silu(z) of the staged elements
+            for (int c = 0; c < CH; ++c) total[c] = both2(0.f);
+        __syncthreads();
+        for (int s = 0; s <= steps; ++s) {
+            if (s < steps) {
+                const float* in = sm + (s & 1) * kIn + lane_place<Gm>(warp, 0, cl) * 4;
+                const float* B0 = sm + (s & 1) * kIn + 4 * LT * CB + 4 * nl;
+                float* o = out + (s & 1) * kOut + lane_place<Gm>(warp, 0, cl) * Gm::NQ + nl;
+#pragma unroll 1
+                for (int tb = 0; tb < LT; tb += Gm::Seg) {
+                    if (MODE == kScanCkpt) {
+                        float* ck = a.ckpt + ((tl.unit * kWalkers + warp) * a.segs + (tl.t0 + s * LT + tb) / Gm::Seg) *
+                                                 Gm::QUADS + lane * 4;
+                        if (tl.t0 + s * LT + tb < tl.n)
 #pragma unroll
-        for (int i = 0; i < Gm::SE; ++i) {
-            const int e = 32 * i + lane, step = e / CPW, ch = e % CPW;
-            const bool on = seg * L + step < tl.n && ch < tl.kleft;
-            const float uf = to_f32(ru[i]), raw = to_f32(rd[i]) + bias[i];
-            const float dt = !on ? 0.f : a.softplus ? softplusf_series(raw) : raw;
-            if (step < L) {
-                sdt[e] = dt;
-                sdtu[e] = dt * uf;
-            }
-            du[i] = skip[i] * uf;
-            gate[i] = 1.f;
-            if (!CKPT && z) {
-                const float zf = to_f32(rz[i]);
-                gate[i] = zf * sigmoidf_fast(zf);
-            }
-        }
-        stage_vecs<T, Gm>(sB, rB, lane);
-        if constexpr (!CKPT) stage_vecs<T, Gm>(sC, rC, lane);
-        __syncwarp();
-        if (seg + kScanWarps < nseg) fetch(seg + kScanWarps);
-
-        f2 h[CH][2], p[CH][2];
-        f2 yv[CKPT ? 1 : L][CH], q[CKPT ? 1 : L][CH][2];
+                            for (int c = 0; c < CH; ++c) sts_quad(ck + c * 128, h[c]);
+                    }
 #pragma unroll
-        for (int t = 0; t < L; ++t) {
-            f2 B[2], C[2];
-            lds_quad(B, sB + t * NP + 4 * nl);
-            if constexpr (!CKPT) lds_quad(C, sC + t * NP + 4 * nl);
-            float dt[CH], dtu[CH];
-            lds_run<CH>(dt, sdt + t * CPW + cl * CH);
-            lds_run<CH>(dtu, sdtu + t * CPW + cl * CH);
+                    for (int i = 0; i < Gm::Seg; ++i) {
+                        const int t = tb + i;
+                        f2 B[2], C[2];
+                        lds_quad(B, B0 + t * NP);
+                        if (MODE == kScanOut) lds_quad(C, B0 + (LT + t) * NP);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const f2 dt2 = pack2(dt[c], dt[c]), dtu2 = pack2(dtu[c], dtu[c]);
+                        for (int c = 0; c < CH; ++c) {
+                            f2 d[2];  // dt, dt u
+                            lds_quad(d, in + (t * CB + c * CL) * 4);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const f2 dec = ex2_pair(mul2(dt2, A[c][k]));
-                    const f2 in = mul2(dtu2, B[k]);
-                    h[c][k] = t == 0 ? in : fma2(dec, h[c][k], in);
-                    p[c][k] = t == 0 ? dec : mul2(p[c][k], dec);
-                    if constexpr (!CKPT) {
-                        yv[t][c] = k == 0 ? mul2(C[k], h[c][k]) : fma2(C[k], h[c][k], yv[t][c]);
-                        q[t][c][k] = mul2(C[k], p[c][k]);
+                            for (int k = 0; k < 2; ++k)
+                                h[c][k] = fma2(ex2_pair(mul2(d[0], A[c][k])), h[c][k], mul2(d[1], B[k]));
+                            if (MODE == kScanEnds) total[c] = add2(total[c], d[0]);
+                            if (MODE == kScanOut) {
+                                const float v = fold_states<Gm>(sum2(fma2(C[1], h[c][1], mul2(C[0], h[c][0]))));
+                                if (nl < Gm::NQ) o[(t * CB + c * CL) * Gm::NQ] = v;
+                            }
+                        }
                     }
                 }
             }
+            __syncthreads();
         }
-        // the state before this segment
-        f2 in[CH][2];
-        if (seg == 0) {
-            if (a.h0) load_states<Gm>(in, a.h0 + sbase, tl, a.N, a.state_vec, cl, nl, 1.f, false);
-            else
+        if (MODE == kScanEnds) {
+            f2 p[CH][2];
 #pragma unroll
-                for (int c = 0; c < CH; ++c) in[c][0] = in[c][1] = pack2(0.f, 0.f);
-        } else {
-            carry_wait(warp);
+            for (int c = 0; c < CH; ++c)
 #pragma unroll
-            for (int c = 0; c < CH; ++c) lds_quad(in[c], carry + warp * Gm::QUADS + (c * 32 + lane) * 4);
+                for (int k = 0; k < 2; ++k) p[c][k] = ex2_pair(mul2(total[c], A[c][k]));
+            store_map<Gm>(a.ends, p, h, a, tl, warp, lane);
         }
+        const int last = max(seq_len(a.lengths, tl.b, a.T) - 1, 0) / a.chunk;
+        if (MODE == kScanOut && a.h_T && tl.part == last) store_states<Gm>(a.h_T, h, a, tl, ch0, nl);
+    } else {
+        const int ht = threadIdx.x - 32 * kWalkers, vch = ht % Gm::VPT * 4;
+        const T* u = reinterpret_cast<const T*>(a.u) + tl.b * a.us[0] + tl.c0;
+        const T* dl = reinterpret_cast<const T*>(a.delta) + tl.b * a.ds[0] + tl.c0;
+        const T* z = MODE == kScanOut && a.z ? reinterpret_cast<const T*>(a.z) + tl.b * a.zs[0] + tl.c0 : nullptr;
+        const T* Bm = reinterpret_cast<const T*>(a.Bm) + tl.b * a.bs[0] + tl.g * a.N;
+        const T* Cm = MODE == kScanOut ? reinterpret_cast<const T*>(a.Cm) + tl.b * a.cs[0] + tl.g * a.N : nullptr;
+        T* y = reinterpret_cast<T*>(a.y) + (size_t)tl.b * a.T * a.D_ + tl.c0 + vch;
+        using Rows = TokenRows<T, Gm, LT>;
+        Rows ru, rd, rz, held_u[2], held_z[2];  // held: of the steps being walked and put out
+        StateRows<T, Gm, LT> rb;
+        float bias[4], skip[4];
+        channel_values(bias, a.bias, tl, vch);
+        channel_values(skip, a.D, tl, vch);
+        auto fetch = [&](int s) {
+            if (s >= steps) return;
+            const int t0 = tl.t0 + s * LT;
+            rd.fetch(dl, a.ds[1], t0, tl, a.act_vec, ht);
+            ru.fetch(u, a.us[1], t0, tl, a.act_vec, ht);
+            rb.fetch(Bm, Cm, a, t0, tl, ht);
+            if (z) rz.fetch(z, a.zs[1], t0, tl, a.act_vec, ht);
+        };
+        auto stage = [&](int s) {
+            if (s >= steps) return;
+            float* in = sm + (s & 1) * kIn;
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+            for (int i = 0; i < Rows::NV; ++i) {
+                const int tok = Rows::token(i, ht);
+                const bool on = tl.t0 + s * LT + tok < tl.n && vch < tl.kleft;
+                float raw[4], uf[4], dt[4];
+                raw_floats(raw, rd.v[i]);
+                raw_floats(uf, ru.v[i]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) h[c][k] = fma2(p[c][k], in[c][k], h[c][k]);
-        if (seg + 1 < nseg) {
-            const int to = (warp + 1) % kScanWarps;
+                for (int j = 0; j < 4; ++j) raw[j] += bias[j];
+                step_sizes(dt, raw, a.softplus);
+                if (tok < LT)
 #pragma unroll
-            for (int c = 0; c < CH; ++c) sts_quad(carry + to * Gm::QUADS + (c * 32 + lane) * 4, h[c]);
-            carry_arrive(to);
-        } else if (!CKPT && a.h_T) {
-            store_states<Gm>(a.h_T + sbase, h, tl, a.N, a.state_vec, cl, nl);
-        }
-        if constexpr (CKPT) {
-            float* ck = a.ckpt + ((size_t)blockIdx.x * a.nseg + seg) * Gm::QUADS;
+                    for (int j = 0; j < 4; ++j) {
+                        const float d = on ? dt[j] : 0.f;
+                        const f2 q[2] = {both2(d), both2(d * uf[j])};
+                        sts_quad(in + (tok * CB + channel_place<Gm>(vch + j)) * 4, q);
+                    }
+            }
+            rb.stage(in + 4 * LT * CB, ht);
+        };
+        fetch(0);
+        stage(0);
+        held_u[1] = ru;
+        held_z[1] = rz;
+        fetch(1);
+        __syncthreads();
+        for (int s = 0; s <= steps; ++s) {
+            stage(s + 1);
+            if (MODE == kScanOut && s > 0) {
+                const float* o = out + ((s - 1) & 1) * kOut;
 #pragma unroll
-            for (int c = 0; c < CH; ++c) sts_quad(ck + (c * 32 + lane) * 4, in[c]);
-        } else {
+                for (int i = 0; i < Rows::NV; ++i) {
+                    const int tok = Rows::token(i, ht), t = tl.t0 + (s - 1) * LT + tok;
+                    if (tok >= LT || t >= tl.t1 || vch >= tl.kleft) continue;
+                    float f[4], uf[4], zf[4];
+                    raw_floats(uf, held_u[0].v[i]);
 #pragma unroll
-            for (int t = 0; t < L; ++t) {
-                float v[CH];
+                    for (int j = 0; j < 4; ++j)
+                        f[j] = fmaf(skip[j], uf[j],
+                                    sum_states<Gm>(o + (tok * CB + channel_place<Gm>(vch + j)) * Gm::NQ));
+                    if (z) {
+                        raw_floats(zf, held_z[0].v[i]);
 #pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    f2 s = fma2(q[t][c][0], in[c][0], yv[t][c]);
-                    s = fma2(q[t][c][1], in[c][1], s);
-                    v[c] = sum2(s);
-                }
-                using Sum = LaneSum<CH, Gm::NS, 1>;
-                Sum::run(v, nl);
-                if (Sum::owner(nl)) {
-#pragma unroll
-                    for (int i = 0; i < Sum::left(); ++i) sy[t * CPW + cl * CH + Sum::first(nl) + i] = v[i];
+                        for (int j = 0; j < 4; j += 2) {
+                            const f2 zz = pack2(zf[j], zf[j + 1]);
+                            unpack2(mul2(mul2(zz, sigmoid2(zz)), pack2(f[j], f[j + 1])), f[j], f[j + 1]);
+                        }
+                    }
+                    if (t >= tl.n) f[0] = f[1] = f[2] = f[3] = 0.f;
+                    store_row(y + (size_t)t * a.D_, f, tl.kleft - vch, a.act_vec);
                 }
             }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < Gm::SE; ++i) {
-                const int e = 32 * i + lane, step = e / CPW, ch = e % CPW, t = seg * L + step;
-                if (step < L && t < a.T && ch < tl.kleft)
-                    y[(size_t)t * a.D_ + ch] = from_f32<T>(t < tl.n ? (sy[e] + du[i]) * gate[i] : 0.f);
-            }
+            held_u[0] = held_u[1];
+            held_z[0] = held_z[1];
+            held_u[1] = ru;
+            held_z[1] = rz;
+            fetch(s + 2);
+            __syncthreads();
         }
-        __syncwarp();
     }
-    if constexpr (!CKPT) {
-        // rows from the last segment on hold no token
-        for (int e = threadIdx.x; e < (a.T - min(a.T, nseg * L)) * CPW; e += kScanThreads) {
-            const int t = nseg * L + e / CPW, ch = e % CPW;
-            if (ch < tl.kleft) y[(size_t)t * a.D_ + ch] = from_f32<T>(0.f);
-        }
-        if (nseg == 0 && warp == 0 && a.h_T) {
-            f2 in[CH][2];
-            if (a.h0) load_states<Gm>(in, a.h0 + sbase, tl, a.N, a.state_vec, cl, nl, 1.f, false);
-            else
-#pragma unroll
-                for (int c = 0; c < CH; ++c) in[c][0] = in[c][1] = pack2(0.f, 0.f);
-            store_states<Gm>(a.h_T + sbase, in, tl, a.N, a.state_vec, cl, nl);
-        }
+    if (MODE == kScanOut) {
+        // rows from the last step on hold no token
+        T* y = reinterpret_cast<T*>(a.y) + (size_t)tl.b * a.T * a.D_ + tl.c0;
+        const int t0 = min(tl.t1, tl.t0 + steps * LT);
+        for (int e = threadIdx.x; e < (tl.t1 - t0) * CB; e += kScanThreads)
+            if (e % CB < tl.kleft) y[(size_t)(t0 + e / CB) * a.D_ + e % CB] = from_f32<T>(0.f);
     }
 }
 
-template <typename T, typename Gm, bool CKPT> static cudaError_t launch_fwd_geom(ScanArgs a, int B, cudaStream_t st) {
-    a.tiles = (a.K + Gm::CPW - 1) / Gm::CPW;
-    const long long grid = (long long)B * a.G * a.tiles;
+template <typename T, int NS, int MODE> static cudaError_t launch_fwd_geom(const ScanArgs& a, int B, cudaStream_t st) {
+    using Gm = ScanGeom<NS>;
+    const long long grid = (long long)B * a.G * a.tiles * a.chunks;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)kScanWarps * (3 * Gm::L * Gm::CPW + 2 * Gm::L * Gm::NP + Gm::QUADS) * sizeof(float);
-    auto kern = scan_fwd_kernel<T, Gm, CKPT>;
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const size_t smem = 2 * (4 * Gm::LT * Gm::CB + 2 * Gm::LT * Gm::NP + Gm::LT * Gm::CB * Gm::NQ) * sizeof(float);
+    auto kern = scan_fwd_kernel<T, Gm, MODE>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, kScanThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
@@ -205,24 +205,42 @@ template <typename F> static cudaError_t dispatch_scan_lanes(int ns, F&& f) {
     }
 }
 
-cudaError_t launch_scan_fwd(const ScanArgs& a, int B, int dtype, cudaStream_t st) {
-    return dispatch_scan_lanes(scan_lanes(a.N), [&](auto nc) {
-        constexpr int NS = decltype(nc)::value;
-        using Gm = ScanGeom<NS, NS == 1 ? 2 : 4, 4>;
-        return dtype == GDR_BF16 ? launch_fwd_geom<__nv_bfloat16, Gm, false>(a, B, st)
-                                 : launch_fwd_geom<float, Gm, false>(a, B, st);
-    });
+// Chunks of the tokens: as many as fill two blocks per SM, of 256 tokens at
+// least, and none below three (see above).
+int scan_chunks(int B, int T, int K, int N, int G) {
+    const long long units = (long long)B * G * scan_tiles(K, N);
+    const long long c = units > 0 ? 296 / units : 0, most = T / 256;
+    const long long n = c < most ? c : most;
+    return n < 3 ? 1 : (int)n;
+}
+// Sets the split; a chunk is a whole number of steps and segments.
+void scan_split(ScanArgs& a, int chunks) {
+    const int per = (a.T + chunks - 1) / chunks;
+    a.chunk = per < 16 ? 16 : (per + 15) / 16 * 16;
+    a.chunks = a.T > 0 ? (a.T + a.chunk - 1) / a.chunk : 1;
+    a.tiles = scan_tiles(a.K, a.N);
+}
+size_t scan_ends_bytes(int B, int G, int K, int N, int chunks) {
+    return chunks < 2 ? 0 : (size_t)B * G * scan_tiles(K, N) * chunks * kWalkers * 2 * 256 * sizeof(float);
 }
 
-// The backward pass's first launch: the state at the start of every segment of
-// its geometry (2 channels per lane, 8 tokens).
-cudaError_t launch_scan_ckpt(const ScanArgs& a, int B, int dtype, cudaStream_t st) {
+template <int MODE> static cudaError_t launch_fwd_mode(const ScanArgs& a, int B, int dtype, cudaStream_t st) {
     return dispatch_scan_lanes(scan_lanes(a.N), [&](auto nc) {
         constexpr int NS = decltype(nc)::value;
-        using Gm = ScanGeom<NS, 2, 8>;
-        return dtype == GDR_BF16 ? launch_fwd_geom<__nv_bfloat16, Gm, true>(a, B, st)
-                                 : launch_fwd_geom<float, Gm, true>(a, B, st);
+        return dtype == GDR_BF16 ? launch_fwd_geom<__nv_bfloat16, NS, MODE>(a, B, st)
+                                 : launch_fwd_geom<float, NS, MODE>(a, B, st);
     });
+}
+cudaError_t launch_scan_fwd(const ScanArgs& a, int B, int dtype, cudaStream_t st) {
+    if (a.chunks > 1) {
+        cudaError_t e = launch_fwd_mode<kScanEnds>(a, B, dtype, st);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_fwd_mode<kScanOut>(a, B, dtype, st);
+}
+// The backward pass's checkpoints: the state at every segment's start.
+cudaError_t launch_scan_ckpt(const ScanArgs& a, int B, int dtype, cudaStream_t st) {
+    return launch_fwd_mode<kScanCkpt>(a, B, dtype, st);
 }
 
 // One token. Bound by HBM: 8 bytes per state, read and written once. A warp
@@ -293,7 +311,7 @@ __global__ void __launch_bounds__(256, kStepBlocks) scan_step_kernel(ScanArgs a,
                     if (n0 + i < a.N) { s[k][i] = hp[ch * a.N + i]; A[k][i] = Ap[ch * a.N + i]; }
             }
         }
-        if (s0 == 0) dt = !own ? 0.f : a.softplus ? softplusf_series(raw) : raw;
+        if (s0 == 0) dt = !own ? 0.f : a.softplus ? softplus1(raw) : raw;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int ch = (s0 + k) * CL + cl;

@@ -7,8 +7,12 @@ cudaError_t launch_scan_fwd(const ScanArgs& a, int B, int dtype, cudaStream_t st
 cudaError_t launch_scan_step(ScanArgs a, float* h, int B, int dtype, cudaStream_t st);
 cudaError_t launch_scan_bwd(ScanArgs a, void* ws, float* dA, float* dB, float* dC, float* dD, float* dbias, int B,
                             int dtype, int grad_dtype, cudaStream_t st);
-struct ScanBwdLayout { size_t ckpt, bc, prm, total; };
-ScanBwdLayout scan_bwd_layout(int B, int T, int D, int N, int G);
+struct ScanBwdLayout { size_t ckpt, bc, prm, ends, grad_ends, total; };
+ScanBwdLayout scan_bwd_layout(int B, int T, int D, int N, int G, int chunks);
+int scan_chunks(int B, int T, int K, int N, int G);
+int scan_bwd_chunks(int B, int T, int K, int N, int G);
+void scan_split(ScanArgs& a, int chunks);
+size_t scan_ends_bytes(int B, int G, int K, int N, int chunks);
 }  // namespace gdr
 
 using namespace gdr;
@@ -39,6 +43,13 @@ static gdr_status scan_fill(ScanArgs& a, const void* u, const void* delta, const
         a.us[i] = s[i]; a.ds[i] = s[2 + i]; a.bs[i] = s[4 + i]; a.cs[i] = s[6 + i]; a.zs[i] = s[8 + i];
         if (with_dy) a.gs[i] = s[10 + i];
     }
+    // wide accesses of 4 elements: B and C, and token rows (the caller adds its outputs)
+    a.bc_vec = N % 4 == 0 && aligned_to(Bm, 4 * e) && aligned_to(Cm, 4 * e);
+    a.act_vec = a.K % 4 == 0 && aligned_to(u, 4 * e) && aligned_to(delta, 4 * e) && aligned_to(z, 4 * e);
+    for (int i = 0; i < 2; ++i) {
+        if (a.bs[i] % 4 || a.cs[i] % 4) a.bc_vec = 0;
+        if (a.us[i] % 4 || a.ds[i] % 4 || (z && a.zs[i] % 4) || a.gs[i] % 4) a.act_vec = 0;
+    }
     return GDR_OK;
 }
 
@@ -54,9 +65,14 @@ static gdr_status launched(cudaError_t e) { return e == cudaSuccess ? GDR_OK : G
 
 extern "C" {
 
+size_t gdr_scan_fwd_workspace_size(int B, int T, int D_, int N, int G) {
+    if (B < 1 || T < 0 || D_ < 1 || N < 1 || N > 128 || G < 1 || D_ % G) return 0;
+    return scan_ends_bytes(B, G, D_ / G, N, scan_chunks(B, T, D_ / G, N, G));
+}
+
 gdr_status gdr_scan_fwd(const void* u, const void* delta, const float* A, const void* Bm, const void* Cm,
                         const float* D, const void* z, const float* delta_bias, const float* h0, const int* lengths,
-                        void* y, float* h_T, const long long* strides, int B, int T, int D_, int N, int G,
+                        void* y, float* h_T, void* workspace, size_t workspace_bytes, const long long* strides, int B, int T, int D_, int N, int G,
                         int delta_softplus, int dtype, void* stream) {
     ScanArgs a;
     gdr_status ok = scan_fill(a, u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, strides, false, B, T, D_, N, G,
@@ -65,13 +81,19 @@ gdr_status gdr_scan_fwd(const void* u, const void* delta, const float* A, const 
     if (T > 0 && !y) return GDR_ERR_INVALID_ARG;
     if (!aligned_to(y, dtype_size(dtype)) || !aligned_to(h_T, 4)) return GDR_ERR_MISALIGNED;
     a.y = y; a.h_T = h_T;
+    a.act_vec = a.act_vec && aligned_to(y, 4 * dtype_size(dtype));
     a.state_vec = states_in_quads(N, {A, h0, h_T});
+    if (workspace && !aligned_to(workspace, 256)) return GDR_ERR_MISALIGNED;
+    const size_t need = gdr_scan_fwd_workspace_size(B, T, D_, N, G);
+    const bool split = workspace && need && workspace_bytes >= need;
+    a.ends = reinterpret_cast<float*>(workspace);
+    scan_split(a, split ? scan_chunks(B, T, a.K, N, G) : 1);
     return launched(launch_scan_fwd(a, B, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t gdr_scan_bwd_workspace_size(int B, int T, int D_, int N, int G) {
     if (B < 1 || T < 0 || D_ < 1 || N < 1 || N > 128 || G < 1 || D_ % G) return 0;
-    return scan_bwd_layout(B, T, D_, N, G).total;
+    return scan_bwd_layout(B, T, D_, N, G, scan_bwd_chunks(B, T, D_ / G, N, G)).total;
 }
 
 gdr_status gdr_scan_bwd(const void* u, const void* delta, const float* A, const void* Bm, const void* Cm,
@@ -98,6 +120,8 @@ gdr_status gdr_scan_bwd(const void* u, const void* delta, const float* A, const 
         if (!aligned_to(p, 4)) return GDR_ERR_MISALIGNED;
     a.dy = dy; a.dh_T = dh_T;
     a.du = du; a.ddelta = ddelta; a.dz = dz; a.dh0 = dh0;
+    a.act_vec = a.act_vec && aligned_to(dy, 4 * dtype_size(grad_dtype)) && aligned_to(du, 16) &&
+                aligned_to(ddelta, 16) && aligned_to(dz, 16);
     a.state_vec = states_in_quads(N, {A, h0, dh_T, dh0});
     return launched(launch_scan_bwd(a, workspace, dA, dB, dC, dD, ddelta_bias, B, dtype, grad_dtype,
                                     reinterpret_cast<cudaStream_t>(stream)));
@@ -118,8 +142,6 @@ gdr_status gdr_scan_step(const void* u, const void* delta, const float* A, const
     if (!aligned_to(y, dtype_size(dtype))) return GDR_ERR_MISALIGNED;
     a.y = y;
     a.state_vec = states_in_quads(N, {A, h});
-    a.bc_vec = N % 4 == 0 && a.bs[0] % 4 == 0 && a.cs[0] % 4 == 0 && aligned_to(Bm, 4 * dtype_size(dtype)) &&
-               aligned_to(Cm, 4 * dtype_size(dtype));
     return launched(launch_scan_step(a, h, B, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -6,16 +6,18 @@
 //   du = dt sum_n g B + D dyh,  d dt = sum_n g (u B + A a h_{t-1})
 //   dA = sum dt a g h_{t-1},  dD = sum dyh u,  dz = dy yh (z sigmoid(z))'
 //   ddelta = d dt sigmoid(delta + bias) (with softplus).
-// Three launches. The forward scan first stores the state at every segment's
-// start (scan.cu). The second walks the segments from the last to the first:
-// a warp rebuilds its segment's states from the stored one (kept in
-// registers) and, with the running decay p, its own contribution to the
-// outgoing state gradient, sum_t p_t C_t dyh_t; the incoming one is then one
-// multiply-add away from the next warp, and the segment is walked back with
-// its decays recomputed (cheaper than holding them: the exponentials run beside
-// the multiply-adds that bound this kernel). dB and dC are summed over a warp's
-// channels by a shuffle reduction; the third launch adds the channel tiles, and
-// the sequences' parameter gradients, in a fixed order.
+// Three launches. The forward scan first stores the state at the start of every
+// segment of 8 tokens (scan.cu). The second walks the segments from the last to
+// the first: a walker rebuilds a segment's states from the stored one, keeping
+// states and decays in registers, and goes back through it. Sums over the states
+// of a channel and over the channels of a block are left to the helpers, through
+// shared memory. The third launch adds the blocks' dB and dC and the sequences'
+// parameter gradients in a fixed order.
+//
+// Where the channels alone leave SMs empty the tokens are split into chunks, as
+// in the forward pass: a launch before the others finds each chunk's maps of its
+// start state (state -> P state + h) and of the gradient that reaches its end
+// (gradient -> P gradient + E, E = sum_t p_t C_t dyh_t with the running decay p).
 #include <type_traits>
 
 #include "scan_common.cuh"
@@ -24,265 +26,338 @@ namespace gdr {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <typename T, typename TG, typename Gm>
+template <typename Gm> struct ScanBwdShared {
+    static constexpr int L = Gm::Seg;
+    // floats of a step: (dt, dt u) quads, dyh pairs, B, C
+    static constexpr int dy = 4 * L * Gm::CB, B = dy + 2 * L * Gm::CB, in = B + 2 * L * Gm::NP;
+    // of its results: sums of C h, g B and A a g h over the states, terms of dB and dC
+    static constexpr int kSum = L * Gm::CB * Gm::NQ, bc = 3 * kSum, out = bc + L * 2 * kWalkers * 128;
+    static constexpr int total = 2 * (in + out);
+};
+
+// ENDS: the chunk's maps only, its segments in order.
+template <typename T, typename TG, typename Gm, bool ENDS>
 __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
-    constexpr int CH = Gm::CH, L = Gm::L, CPW = Gm::CPW, NP = Gm::NP, NS = Gm::NS;
-    static_assert(CH == 2, "channels of a lane");
+    constexpr int CH = Gm::CH, L = Gm::Seg, CB = Gm::CB, CL = Gm::CL, NP = Gm::NP, NS = Gm::NS, NQ = Gm::NQ;
+    using Sh = ScanBwdShared<Gm>;
     extern __shared__ __align__(16) float sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nl = lane % NS, cl = lane / NS;
-    constexpr int kRows = 6;  // dt, dt u, dyh; sums of C h, g B, A a g h
-    constexpr int kWarpFloats = kRows * L * CPW + 2 * L * NP;
-    float* sdt = sm + warp * kWarpFloats;
-    float* sdtu = sdt + L * CPW;
-    float* sdy = sdtu + L * CPW;
-    float* sY = sdy + L * CPW;
-    float* sGB = sY + L * CPW;
-    float* sDD = sGB + L * CPW;
-    float* sB = sDD + L * CPW;
-    float* sC = sB + L * NP;
-    float* carry = sm + kScanWarps * kWarpFloats;
-    const ScanTile tl(a, CPW);
-    const T* u = reinterpret_cast<const T*>(a.u) + tl.b * a.us[0] + tl.c0;
-    const T* dl = reinterpret_cast<const T*>(a.delta) + tl.b * a.ds[0] + tl.c0;
-    const T* z = a.z ? reinterpret_cast<const T*>(a.z) + tl.b * a.zs[0] + tl.c0 : nullptr;
-    const TG* dy = reinterpret_cast<const TG*>(a.dy) + tl.b * a.gs[0] + tl.c0;
-    const T* Bm = reinterpret_cast<const T*>(a.Bm) + tl.b * a.bs[0] + tl.g * a.N;
-    const T* Cm = reinterpret_cast<const T*>(a.Cm) + tl.b * a.cs[0] + tl.g * a.N;
-    const size_t rbase = (size_t)tl.b * a.T * a.D_ + tl.c0, sbase = (size_t)tl.b * a.D_ * a.N;
-    float* bcp = a.bcpart + (((size_t)tl.tile * (gridDim.x / (a.tiles * a.G)) + tl.b) * a.T * a.G + tl.g) * (2 * NP);
-    const int nseg = (tl.n + L - 1) / L;
+    const ScanTile tl(a, CB);
+    const int steps = (tl.n - tl.t0 + L - 1) / L;
+    float* const results = sm + 2 * Sh::in;
+    auto segment = [&](int s) { return ENDS ? s : steps - 1 - s; };  // of step s
+    float* const prm = a.prm + ((size_t)tl.b * a.chunks + tl.part) * a.D_ * (a.N + 2);
 
-    f2 A[CH][2], dA[CH][2];
-    load_states<Gm>(A, a.A, tl, a.N, a.state_vec, cl, nl, kLog2e, true);
+    if (warp < kWalkers) {
+        const int nl = lane % NS, cl = lane / NS, ch0 = warp * Gm::CPW + cl * CH, at0 = lane_place<Gm>(warp, 0, cl);
+        f2 A[CH][2];
+        load_states<Gm>(A, a.A, tl, a.N, a.state_vec, ch0, nl, kLog2e, true);
+        if constexpr (ENDS) {
+            f2 h[CH][2], p[CH][2], E[CH][2];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) dA[c][0] = dA[c][1] = pack2(0.f, 0.f);
-    constexpr int AC = CPW > 32 ? CPW / 32 : 1;  // channels of a lane's staged elements
-    float bias[AC], skip[AC], dD[AC], db[AC];
-#pragma unroll
-    for (int i = 0; i < AC; ++i) {
-        const int ch = (32 * i + lane) % CPW;
-        bias[i] = a.bias && ch < tl.kleft ? a.bias[tl.c0 + ch] : 0.f;
-        skip[i] = a.D && ch < tl.kleft ? a.D[tl.c0 + ch] : 0.f;
-        dD[i] = db[i] = 0.f;
-    }
-    T ru[Gm::SE], rd[Gm::SE], rz[Gm::SE], rB[Gm::BE], rC[Gm::BE];
-    TG rg[Gm::SE];
-    auto fetch = [&](int seg) {
-        fetch_rows<T, Gm>(ru, u, a.us[1], seg * L, tl, lane);
-        fetch_rows<T, Gm>(rd, dl, a.ds[1], seg * L, tl, lane);
-        if (z) fetch_rows<T, Gm>(rz, z, a.zs[1], seg * L, tl, lane);
-        fetch_rows<TG, Gm>(rg, dy, a.gs[1], seg * L, tl, lane);
-        fetch_vecs<T, Gm>(rB, Bm, a.bs[1], seg * L, tl, a.N, lane);
-        fetch_vecs<T, Gm>(rC, Cm, a.cs[1], seg * L, tl, a.N, lane);
-    };
-    // warp w takes the segments nseg - 1 - w, nseg - 1 - w - kScanWarps, ...
-    if (nseg - 1 - warp >= 0) fetch(nseg - 1 - warp);
-    for (int seg = nseg - 1 - warp; seg >= 0; seg -= kScanWarps) {
-        float uf[Gm::SE], sig[Gm::SE], gz[Gm::SE];  // u, ddt/ddelta, dy dgate/dz
-        const float* ck = a.ckpt + ((size_t)blockIdx.x * a.nseg + seg) * Gm::QUADS;
-        f2 h0[CH][2];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) lds_quad(h0[c], ck + (c * 32 + lane) * 4);
-#pragma unroll
-        for (int i = 0; i < Gm::SE; ++i) {
-            const int e = 32 * i + lane, step = e / CPW, ch = e % CPW;
-            const bool on = seg * L + step < tl.n && ch < tl.kleft;
-            uf[i] = to_f32(ru[i]);
-            const float raw = to_f32(rd[i]) + bias[i % AC];
-            const float dt = !on ? 0.f : a.softplus ? softplusf_series(raw) : raw;
-            sig[i] = !on ? 0.f : a.softplus ? sigmoidf_fast(raw) : 1.f;
-            float dyh = to_f32(rg[i]);
-            gz[i] = 0.f;
-            if (z) {
-                const float zf = to_f32(rz[i]), sg = sigmoidf_fast(zf);
-                gz[i] = on ? dyh * (sg * fmaf(zf, 1.f - sg, 1.f)) : 0.f;
-                dyh = on ? dyh * (zf * sg) : 0.f;
-            }
-            if (step < L) {
-                sdt[e] = dt;
-                sdtu[e] = dt * uf[i];
-                sdy[e] = dyh;
-            }
-        }
-        stage_vecs<T, Gm>(sB, rB, lane);
-        stage_vecs<T, Gm>(sC, rC, lane);
-        __syncwarp();
-        if (seg - kScanWarps >= 0) fetch(seg - kScanWarps);
-
-        // forward through the segment: states, running decay, and the
-        // segment's own part of the outgoing gradient
-        f2 h[L][CH][2], p[CH][2], E[CH][2];
-#pragma unroll
-        for (int t = 0; t < L; ++t) {
-            f2 B[2], C[2];
-            lds_quad(B, sB + t * NP + 4 * nl);
-            lds_quad(C, sC + t * NP + 4 * nl);
-            float dt[CH], dtu[CH], dyh[CH];
-            lds_run<CH>(dt, sdt + t * CPW + cl * CH);
-            lds_run<CH>(dtu, sdtu + t * CPW + cl * CH);
-            lds_run<CH>(dyh, sdy + t * CPW + cl * CH);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const f2 dt2 = pack2(dt[c], dt[c]), dtu2 = pack2(dtu[c], dtu[c]), dy2 = pack2(dyh[c], dyh[c]);
+            for (int c = 0; c < CH; ++c)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const f2 dec = ex2_pair(mul2(dt2, A[c][k]));
-                    h[t][c][k] = fma2(dec, t == 0 ? h0[c][k] : h[t - 1][c][k], mul2(dtu2, B[k]));
-                    p[c][k] = t == 0 ? dec : mul2(p[c][k], dec);
-                    const f2 cd = mul2(C[k], dy2);
-                    E[c][k] = t == 0 ? mul2(p[c][k], cd) : fma2(p[c][k], cd, E[c][k]);
+                    h[c][k] = E[c][k] = both2(0.f);
+                    p[c][k] = both2(1.f);
                 }
+            __syncthreads();
+            for (int s = 0; s <= steps; ++s) {
+                const float* in = sm + (s & 1) * Sh::in;
+                if (s < steps) {
+#pragma unroll
+                    for (int t = 0; t < L; ++t) {
+                        f2 B[2], C[2];
+                        lds_quad(B, in + Sh::B + t * NP + 4 * nl);
+                        lds_quad(C, in + Sh::B + (L + t) * NP + 4 * nl);
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            const int at = t * CB + c * CL + at0;
+                            f2 d[2];
+                            lds_quad(d, in + at * 4);
+                            const f2 dyh = *reinterpret_cast<const f2*>(in + Sh::dy + at * 2);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const f2 e = ex2_pair(mul2(d[0], A[c][k]));
+                                h[c][k] = fma2(e, h[c][k], mul2(d[1], B[k]));
+                                p[c][k] = mul2(p[c][k], e);
+                                E[c][k] = fma2(p[c][k], mul2(C[k], dyh), E[c][k]);
+                            }
+                        }
+                    }
+                }
+                __syncthreads();
             }
-        }
-        // the gradient that reaches the segment's last state from later ones
-        f2 g[CH][2];
-        if (seg == nseg - 1) {
-            if (a.dh_T) load_states<Gm>(g, a.dh_T + sbase, tl, a.N, a.state_vec, cl, nl, 1.f, false);
-            else
-#pragma unroll
-                for (int c = 0; c < CH; ++c) g[c][0] = g[c][1] = pack2(0.f, 0.f);
+            store_map<Gm>(a.ends, p, h, a, tl, warp, lane);
+            store_map<Gm>(a.grad_ends, p, E, a, tl, warp, lane);
         } else {
-            carry_wait(warp);
+            f2 dA[CH][2], g[CH][2], next[CH][2];
+            load_given<Gm>(g, a.dh_T, a, tl, ch0, nl);
+            fold_chunks<Gm>(g, a.grad_ends, a, tl, warp, lane, a.chunks - 1, tl.part, -1);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) lds_quad(g[c], carry + warp * Gm::QUADS + (c * 32 + lane) * 4);
-        }
+            for (int c = 0; c < CH; ++c) dA[c][0] = dA[c][1] = both2(0.f);
+            const float* ckpt = a.ckpt + ((tl.unit * kWalkers + warp) * a.segs + tl.t0 / L) * Gm::QUADS + lane * 4;
+            auto fetch = [&](int s) {
+                if (s >= steps) return;
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+                for (int c = 0; c < CH; ++c) lds_quad(next[c], ckpt + (size_t)segment(s) * Gm::QUADS + c * 128);
+            };
+            fetch(0);
+            __syncthreads();
+            for (int s = 0; s <= steps; ++s) {
+                if (s < steps) {
+                    const float* in = sm + (s & 1) * Sh::in;
+                    float* o = results + (s & 1) * Sh::out;
+                    f2 h0[CH][2], h[L][CH][2], dec[L][CH][2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) E[c][k] = fma2(p[c][k], g[c][k], E[c][k]);
-        if (seg > 0) {
-            const int to = (warp + 1) % kScanWarps;
+                    for (int c = 0; c < CH; ++c) {
+                        h0[c][0] = next[c][0];
+                        h0[c][1] = next[c][1];
+                    }
+                    fetch(s + 1);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) sts_quad(carry + to * Gm::QUADS + (c * 32 + lane) * 4, E[c]);
-            carry_arrive(to);
-        } else if (a.dh0) {
-            store_states<Gm>(a.dh0 + sbase, E, tl, a.N, a.state_vec, cl, nl);
-        }
-        // back through the segment
+                    for (int t = 0; t < L; ++t) {
+                        f2 B[2];
+                        lds_quad(B, in + Sh::B + t * NP + 4 * nl);
 #pragma unroll
-        for (int t = L - 1; t >= 0; --t) {
-            f2 B[2], C[2], dB[2], dC[2];
-            lds_quad(B, sB + t * NP + 4 * nl);
-            lds_quad(C, sC + t * NP + 4 * nl);
-            float dt[CH], dtu[CH], dyh[CH], v[3 * CH];
-            lds_run<CH>(dt, sdt + t * CPW + cl * CH);
-            lds_run<CH>(dtu, sdtu + t * CPW + cl * CH);
-            lds_run<CH>(dyh, sdy + t * CPW + cl * CH);
+                        for (int c = 0; c < CH; ++c) {
+                            f2 d[2];
+                            lds_quad(d, in + (t * CB + c * CL + at0) * 4);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                dec[t][c][k] = ex2_pair(mul2(d[0], A[c][k]));
+                                h[t][c][k] = fma2(dec[t][c][k], t == 0 ? h0[c][k] : h[t - 1][c][k], mul2(d[1], B[k]));
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int t = L - 1; t >= 0; --t) {
+                        f2 B[2], C[2], dB[2], dC[2];
+                        lds_quad(B, in + Sh::B + t * NP + 4 * nl);
+                        lds_quad(C, in + Sh::B + (L + t) * NP + 4 * nl);
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            const int at = t * CB + c * CL + at0;
+                            f2 d[2], yc, gB, dd;
+                            lds_quad(d, in + at * 4);
+                            const f2 dyh = *reinterpret_cast<const f2*>(in + Sh::dy + at * 2);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const f2 gt = fma2(C[k], dyh, g[c][k]), ht = h[t][c][k];
+                                yc = k == 0 ? mul2(C[k], ht) : fma2(C[k], ht, yc);
+                                gB = k == 0 ? mul2(B[k], gt) : fma2(B[k], gt, gB);
+                                dB[k] = c == 0 ? mul2(gt, d[1]) : fma2(gt, d[1], dB[k]);
+                                dC[k] = c == 0 ? mul2(ht, dyh) : fma2(ht, dyh, dC[k]);
+                                g[c][k] = mul2(dec[t][c][k], gt);
+                                const f2 w = mul2(g[c][k], t == 0 ? h0[c][k] : h[t - 1][c][k]);
+                                dA[c][k] = fma2(w, d[0], dA[c][k]);
+                                dd = k == 0 ? mul2(A[c][k], w) : fma2(A[c][k], w, dd);  // A log2(e) here
+                            }
+                            const float vy = fold_states<Gm>(sum2(yc)), vg = fold_states<Gm>(sum2(gB)),
+                                        vd = fold_states<Gm>(sum2(dd));
+                            if (nl < NQ) {
+                                o[at * NQ + nl] = vy;
+                                o[Sh::kSum + at * NQ + nl] = vg;
+                                o[2 * Sh::kSum + at * NQ + nl] = vd;
+                            }
+                        }
+                        sts_quad(o + Sh::bc + ((2 * t) * kWalkers + warp) * 128 + lane * 4, dB);
+                        sts_quad(o + Sh::bc + ((2 * t + 1) * kWalkers + warp) * 128 + lane * 4, dC);
+                    }
+                }
+                __syncthreads();
+            }
+            if (a.dh0 && tl.part == 0) store_states<Gm>(a.dh0, g, a, tl, ch0, nl);
+            // dA: this block's part, a lane's own states
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                const f2 dt2 = pack2(dt[c], dt[c]), dtu2 = pack2(dtu[c], dtu[c]), dy2 = pack2(dyh[c], dyh[c]);
-                f2 yc, gB, dd;
+                float f[4];
+                unpack2(dA[c][0], f[0], f[1]);
+                unpack2(dA[c][1], f[2], f[3]);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const f2 dec = ex2_pair(mul2(dt2, A[c][k]));
-                    const f2 gt = fma2(C[k], dy2, g[c][k]), ht = h[t][c][k];
-                    yc = k == 0 ? mul2(C[k], ht) : fma2(C[k], ht, yc);
-                    gB = k == 0 ? mul2(B[k], gt) : fma2(B[k], gt, gB);
-                    dB[k] = c == 0 ? mul2(gt, dtu2) : fma2(gt, dtu2, dB[k]);
-                    dC[k] = c == 0 ? mul2(ht, dy2) : fma2(ht, dy2, dC[k]);
-                    g[c][k] = mul2(dec, gt);
-                    const f2 w = mul2(g[c][k], t == 0 ? h0[c][k] : h[t - 1][c][k]);
-                    dA[c][k] = fma2(w, dt2, dA[c][k]);
-                    dd = k == 0 ? mul2(A[c][k], w) : fma2(A[c][k], w, dd);  // A log2(e) here
-                }
-                v[3 * c] = sum2(yc);
-                v[3 * c + 1] = sum2(gB);
-                v[3 * c + 2] = sum2(dd);
-            }
-            // over the states: values 3 c + {y, gB, dd}
-            using Sum = LaneSum<3 * CH, NS, 1>;
-            Sum::run(v, nl);
-            if (Sum::owner(nl)) {
-#pragma unroll
-                for (int i = 0; i < Sum::left(); i += 3) {
-                    const int at = t * CPW + cl * CH + (Sum::first(nl) + i) / 3;
-                    sY[at] = v[i];
-                    sGB[at] = v[i + 1];
-                    sDD[at] = v[i + 2] * kLn2;
-                }
-            }
-            // over the warp's channels: 4 states of dB, then of dC
-            float w[8];
-            unpack2(dB[0], w[0], w[1]);
-            unpack2(dB[1], w[2], w[3]);
-            unpack2(dC[0], w[4], w[5]);
-            unpack2(dC[1], w[6], w[7]);
-            using Bc = LaneSum<8, Gm::CL, NS>;
-            Bc::run(w, lane);
-            const int tok = seg * L + t;
-            if (tok < tl.n && Bc::owner(lane)) {
-                float* o = bcp + (size_t)tok * a.G * (2 * NP);
-#pragma unroll
-                for (int i = 0; i < Bc::left(); ++i) {
-                    const int e = Bc::first(lane) + i;
-                    o[(e >> 2) * NP + 4 * nl + (e & 3)] = w[i];
-                }
+                for (int i = 0; i < 4; ++i)
+                    if (ch0 + c < tl.kleft && nl * 4 + i < a.N) prm[(size_t)(tl.c0 + ch0 + c) * a.N + nl * 4 + i] = f[i];
             }
         }
-        __syncwarp();
+    } else {
+        const int ht = threadIdx.x - 32 * kWalkers, vch = ht % Gm::VPT * 4;
+        const T* u = reinterpret_cast<const T*>(a.u) + tl.b * a.us[0] + tl.c0;
+        const T* dl = reinterpret_cast<const T*>(a.delta) + tl.b * a.ds[0] + tl.c0;
+        const T* z = a.z ? reinterpret_cast<const T*>(a.z) + tl.b * a.zs[0] + tl.c0 : nullptr;
+        const TG* dy = reinterpret_cast<const TG*>(a.dy) + tl.b * a.gs[0] + tl.c0;
+        const T* Bm = reinterpret_cast<const T*>(a.Bm) + tl.b * a.bs[0] + tl.g * a.N;
+        const T* Cm = reinterpret_cast<const T*>(a.Cm) + tl.b * a.cs[0] + tl.g * a.N;
+        const size_t rbase = (size_t)tl.b * a.T * a.D_ + tl.c0 + vch;
+        float* bcp = a.bcpart + (((size_t)tl.tile * (gridDim.x / (a.tiles * a.chunks * a.G)) + tl.b) * a.T * a.G + tl.g) * (2 * NP);
+        using Rows = TokenRows<T, Gm, L>;
+        Rows ru, rd, rz, held_u[2];  // held: of the segments being walked and put out
+        TokenRows<TG, Gm, L> rg;
+        StateRows<T, Gm, L> rb;
+        float sig[Rows::NV][4], gz[Rows::NV][4], held_sig[Rows::NV][4], held_gz[Rows::NV][4];  // ddt/ddelta, dy dgate/dz
+        float bias[4], skip[4], dD[4] = {0.f, 0.f, 0.f, 0.f}, db[4] = {0.f, 0.f, 0.f, 0.f};
+        channel_values(bias, a.bias, tl, vch);
+        channel_values(skip, a.D, tl, vch);
+        auto fetch = [&](int s) {
+            if (s >= steps) return;
+            const int t0 = tl.t0 + segment(s) * L;
+            rd.fetch(dl, a.ds[1], t0, tl, a.act_vec, ht);
+            ru.fetch(u, a.us[1], t0, tl, a.act_vec, ht);
+            rb.fetch(Bm, Cm, a, t0, tl, ht);
+            rg.fetch(dy, a.gs[1], t0, tl, a.act_vec, ht);
+            if (z) rz.fetch(z, a.zs[1], t0, tl, a.act_vec, ht);
+        };
+        auto stage = [&](int s) {
+            if (s >= steps) return;
+            float* in = sm + (s & 1) * Sh::in;
 #pragma unroll
-        for (int i = 0; i < Gm::SE; ++i) {
-            const int e = 32 * i + lane, step = e / CPW, ch = e % CPW, t = seg * L + step;
-            if (step >= L || t >= a.T || ch >= tl.kleft) continue;
-            const float dyh = sdy[e], gB = sGB[e];
-            const bool on = t < tl.n;
-            const float dd = on ? fmaf(uf[i], gB, sDD[e]) * sig[i] : 0.f;
-            const size_t o = rbase + (size_t)t * a.D_ + ch;
-            a.du[o] = on ? fmaf(sdt[e], gB, skip[i % AC] * dyh) : 0.f;
-            a.ddelta[o] = dd;
-            if (z) a.dz[o] = on ? gz[i] * fmaf(skip[i % AC], uf[i], sY[e]) : 0.f;
-            dD[i % AC] = fmaf(dyh, uf[i], dD[i % AC]);
-            db[i % AC] += dd;
+            for (int i = 0; i < Rows::NV; ++i) {
+                const int tok = Rows::token(i, ht);
+                const bool on = tl.t0 + segment(s) * L + tok < tl.n && vch < tl.kleft;
+                float raw[4], uf[4], dt[4], g[4];
+                raw_floats(raw, rd.v[i]);
+                raw_floats(uf, ru.v[i]);
+                raw_floats(g, rg.v[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) raw[j] += bias[j];
+                step_sizes(dt, raw, a.softplus);
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                    if (!ENDS) {
+                        f2 sg = both2(1.f);
+                        if (a.softplus) sg = sigmoid2(pack2(raw[j], raw[j + 1]));
+                        unpack2(sg, sig[i][j], sig[i][j + 1]);
+                    }
+                    if (z) {
+                        float z0 = rz.v[i].get(j), z1 = rz.v[i].get(j + 1);
+                        const f2 zz = pack2(z0, z1), sz = sigmoid2(zz), gg = pack2(g[j], g[j + 1]);
+                        // (z s)' = s (1 + z (1 - s))
+                        if (!ENDS)
+                            unpack2(mul2(gg, mul2(sz, fma2(zz, fma2(sz, both2(-1.f), both2(1.f)), both2(1.f)))),
+                                    gz[i][j], gz[i][j + 1]);
+                        unpack2(mul2(gg, mul2(zz, sz)), g[j], g[j + 1]);
+                    }
+                }
+                if (tok < L)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float d = on ? dt[j] : 0.f;
+                        const f2 q[2] = {both2(d), both2(d * uf[j])};
+                        const int at = tok * CB + channel_place<Gm>(vch + j);
+                        sts_quad(in + at * 4, q);
+                        *reinterpret_cast<f2*>(in + Sh::dy + at * 2) = both2(on ? g[j] : 0.f);
+                    }
+            }
+            rb.stage(in + Sh::B, ht);
+        };
+        auto put_out = [&](int s) {
+            const float* in = sm + (s & 1) * Sh::in;
+            const float* o = results + (s & 1) * Sh::out;
+            const int t0 = tl.t0 + segment(s) * L;
+#pragma unroll
+            for (int i = 0; i < Rows::NV; ++i) {
+                const int tok = Rows::token(i, ht), t = t0 + tok;
+                if (tok >= L || t >= tl.t1 || vch >= tl.kleft) continue;
+                float uf[4], du[4], dd[4], dz[4];
+                raw_floats(uf, held_u[0].v[i]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int at = tok * CB + channel_place<Gm>(vch + j);
+                    const float dt = in[at * 4], dyh = in[Sh::dy + at * 2];
+                    const float gB = sum_states<Gm>(o + Sh::kSum + at * NQ);
+                    const float sd = sum_states<Gm>(o + 2 * Sh::kSum + at * NQ) * kLn2;
+                    du[j] = fmaf(dt, gB, skip[j] * dyh);
+                    dd[j] = fmaf(uf[j], gB, sd) * held_sig[i][j];
+                    if (z) dz[j] = held_gz[i][j] * fmaf(skip[j], uf[j], sum_states<Gm>(o + at * NQ));
+                    if (t >= tl.n) du[j] = dd[j] = dz[j] = 0.f;
+                    dD[j] = fmaf(dyh, uf[j], dD[j]);
+                    db[j] += dd[j];
+                }
+                const size_t row = rbase + (size_t)t * a.D_;
+                store_row(a.du + row, du, tl.kleft - vch, a.act_vec);
+                store_row(a.ddelta + row, dd, tl.kleft - vch, a.act_vec);
+                if (z) store_row(a.dz + row, dz, tl.kleft - vch, a.act_vec);
+            }
+            // dB, dC over the block's channels: quad e is token e / (2 NS), B or C, 4
+            // states; F threads add up to 4 CL terms, each row from another lane on
+            // (for the banks)
+            constexpr int Q = L * 2 * NS, F = Q < kHelperThreads ? kHelperThreads / Q : 1, kTerms = kWalkers * CL / F;
+#pragma unroll
+            for (int q0 = 0; q0 < Q; q0 += kHelperThreads / F) {
+                const int e = q0 + ht / F, row = e / NS, first = ht % F * kTerms, t = t0 + row / 2;
+                f2 v[2] = {both2(0.f), both2(0.f)};
+#pragma unroll
+                for (int k = 0; k < kTerms; ++k) {
+                    const int term = first + k;
+                    f2 x[2];
+                    lds_quad(x, o + Sh::bc + (row * kWalkers + term / CL) * 128 + ((term + row) % CL * NS + e % NS) * 4);
+                    v[0] = add2(v[0], x[0]);
+                    v[1] = add2(v[1], x[1]);
+                }
+#pragma unroll
+                for (int m = 1; m < F; m <<= 1) {
+                    v[0] = add2(v[0], __shfl_xor_sync(0xffffffffu, v[0], m));
+                    v[1] = add2(v[1], __shfl_xor_sync(0xffffffffu, v[1], m));
+                }
+                if (ht % F == 0 && t < tl.n) sts_quad(bcp + (size_t)t * a.G * (2 * NP) + (row & 1) * NP + e % NS * 4, v);
+            }
+        };
+        auto hold = [&]() {
+            held_u[0] = held_u[1];
+            held_u[1] = ru;
+        };
+        float sig1[Rows::NV][4], gz1[Rows::NV][4];  // of the segment being walked
+        auto hold_factors = [&]() {
+#pragma unroll
+            for (int i = 0; i < Rows::NV; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    held_sig[i][j] = sig1[i][j];
+                    held_gz[i][j] = gz1[i][j];
+                    sig1[i][j] = sig[i][j];
+                    gz1[i][j] = gz[i][j];
+                }
+        };
+        fetch(0);
+        stage(0);
+        hold();
+        if (!ENDS) hold_factors();
+        fetch(1);
+        __syncthreads();
+        for (int s = 0; s <= steps; ++s) {
+            if (!ENDS && s > 0) put_out(s - 1);
+            stage(s + 1);
+            if (!ENDS) {
+                hold();
+                hold_factors();
+            }
+            fetch(s + 2);
+            __syncthreads();
         }
-        __syncwarp();
-    }
-    // rows that hold no token
-    for (int e = threadIdx.x; e < (a.T - min(a.T, nseg * L)) * CPW; e += kScanThreads) {
-        const int t = nseg * L + e / CPW, ch = e % CPW;
-        if (ch >= tl.kleft) continue;
-        const size_t o = rbase + (size_t)t * a.D_ + ch;
-        a.du[o] = a.ddelta[o] = 0.f;
-        if (z) a.dz[o] = 0.f;
-    }
-    if (nseg == 0 && warp == 0 && a.dh0) {
-        f2 g[CH][2];
-        if (a.dh_T) load_states<Gm>(g, a.dh_T + sbase, tl, a.N, a.state_vec, cl, nl, 1.f, false);
-        else
+        if constexpr (!ENDS) {
+            // rows that hold no token
+            const int t0 = min(tl.t1, tl.t0 + steps * L);
+            for (int e = ht; e < (tl.t1 - t0) * CB; e += kHelperThreads) {
+                if (e % CB >= tl.kleft) continue;
+                const size_t o = rbase - vch + (size_t)(t0 + e / CB) * a.D_ + e % CB;
+                a.du[o] = a.ddelta[o] = 0.f;
+                if (z) a.dz[o] = 0.f;
+            }
+            // dD, ddelta_bias: threads of a channel added in order
+            constexpr int kShare = kHelperThreads / Gm::VPT;
+            float* red = sm;  // [dD, db][share][CB]
 #pragma unroll
-            for (int c = 0; c < CH; ++c) g[c][0] = g[c][1] = pack2(0.f, 0.f);
-        store_states<Gm>(a.dh0 + sbase, g, tl, a.N, a.state_vec, cl, nl);
-    }
-    // the sequence's parameter gradients: warps added in order
-    __syncthreads();
-    float* red = sm;  // [warp][QUADS + 2 CPW]
-    constexpr int kRed = Gm::QUADS + 2 * CPW;
+            for (int j = 0; j < 4; ++j) {
+                red[ht / Gm::VPT * CB + vch + j] = dD[j];
+                red[(kShare + ht / Gm::VPT) * CB + vch + j] = db[j];
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(kHelperThreads) : "memory");
+            for (int e = ht; e < 2 * CB; e += kHelperThreads) {
+                const int which = e / CB, ch = e % CB;
+                float v = 0.f;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) sts_quad(red + warp * kRed + (c * 32 + lane) * 4, dA[c]);
-#pragma unroll
-    for (int i = 0; i < AC; ++i) {
-#pragma unroll
-        for (int m = CPW; m < 32; m <<= 1) {
-            dD[i] += __shfl_xor_sync(0xffffffffu, dD[i], m);
-            db[i] += __shfl_xor_sync(0xffffffffu, db[i], m);
-        }
-        if (lane < CPW) {
-            red[warp * kRed + Gm::QUADS + 32 * i + lane] = dD[i];
-            red[warp * kRed + Gm::QUADS + CPW + 32 * i + lane] = db[i];
-        }
-    }
-    __syncthreads();
-    float* prm = a.prm + (size_t)tl.b * a.D_ * (a.N + 2);
-    for (int e = threadIdx.x; e < kRed; e += kScanThreads) {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < kScanWarps; ++w) s += red[w * kRed + e];
-        if (e < Gm::QUADS) {
-            const int ln = (e >> 2) & 31, ch = (ln / NS) * CH + (e >> 7), n = (ln % NS) * 4 + (e & 3);
-            if (ch < tl.kleft && n < a.N) prm[(size_t)(tl.c0 + ch) * a.N + n] = s;
-        } else {
-            const int r = e - Gm::QUADS, ch = r % CPW;
-            if (ch < tl.kleft) prm[(size_t)a.D_ * (a.N + r / CPW) + tl.c0 + ch] = s;
+                for (int k = 0; k < kShare; ++k) v += red[(which * kShare + k) * CB + ch];
+                if (ch < tl.kleft) prm[(size_t)a.D_ * (a.N + which) + tl.c0 + ch] = v;
+            }
         }
     }
 }
@@ -294,7 +369,7 @@ struct ScanReduce {
     const int* lengths;
     float *dB, *dC, *dA, *dD, *dbias;
     long long vecs;  // B * T * G
-    int B, T, G, D_, N, NP, tiles;
+    int T, G, D_, N, NP, tiles, parts;  // parts: sequences x chunks
     unsigned bc_blocks;
 };
 
@@ -317,75 +392,94 @@ __global__ void __launch_bounds__(256) scan_reduce_kernel(ScanReduce r) {
     const long long da = (long long)r.D_ * r.N, all = da + 2ll * r.D_;
     if (e >= all) return;
     float s = 0.f;
-    for (int b = 0; b < r.B; ++b) s += r.prm[(size_t)b * all + e];
+    for (int b = 0; b < r.parts; ++b) s += r.prm[(size_t)b * all + e];
     if (e < da) r.dA[e] = s;
     else if (e < da + r.D_) { if (r.dD) r.dD[e - da] = s; }
     else if (r.dbias) r.dbias[e - da - r.D_] = s;
 }
 
 cudaError_t launch_scan_ckpt(const ScanArgs& a, int B, int dtype, cudaStream_t st);
+void scan_split(ScanArgs& a, int chunks);
+size_t scan_ends_bytes(int B, int G, int K, int N, int chunks);
 
-// Channels per tile of the backward geometry (2 per lane).
-static int bwd_tiles(int K, int N) { const int cpw = 64 / scan_lanes(N); return (K + cpw - 1) / cpw; }
-constexpr int kBwdL = 8;
+// Chunks of the backward pass: its blocks run one to an SM; the maps cost a
+// third walk beside two, so two chunks pay already.
+int scan_bwd_chunks(int B, int T, int K, int N, int G) {
+    const long long units = (long long)B * G * scan_tiles(K, N);
+    const long long c = units > 0 ? 148 / units : 0, most = T / 256;
+    const long long n = c < most ? c : most;
+    return n < 2 ? 1 : (int)n;
+}
 
-struct ScanBwdLayout { size_t ckpt, bc, prm, total; };
-ScanBwdLayout scan_bwd_layout(int B, int T, int D, int N, int G) {
-    const size_t tiles = bwd_tiles(D / G, N), np = 4 * scan_lanes(N);
+static int bwd_segments(int T, int N) { const int l = scan_lanes(N) == 1 ? 4 : 8; return (T + l - 1) / l; }
+
+struct ScanBwdLayout { size_t ckpt, bc, prm, ends, grad_ends, total; };
+ScanBwdLayout scan_bwd_layout(int B, int T, int D, int N, int G, int chunks) {
+    const size_t tiles = scan_tiles(D / G, N), np = 4 * scan_lanes(N), ends = scan_ends_bytes(B, G, D / G, N, chunks);
     ScanBwdLayout l;
     l.ckpt = 0;
-    l.bc = l.ckpt + round256((size_t)B * G * tiles * ((T + kBwdL - 1) / kBwdL) * (2 * 32 * 4) * sizeof(float));
+    l.bc = l.ckpt + round256((size_t)B * G * tiles * kWalkers * bwd_segments(T, N) * 256 * sizeof(float));
     l.prm = l.bc + round256(tiles * B * T * G * 2 * np * sizeof(float));
-    l.total = l.prm + round256((size_t)B * D * (N + 2) * sizeof(float));
+    l.ends = l.prm + round256((size_t)B * chunks * D * (N + 2) * sizeof(float));
+    l.grad_ends = l.ends + ends;
+    l.total = l.grad_ends + ends;
     return l;
 }
 
-template <typename T, typename TG, int NS> static cudaError_t launch_bwd_geom(ScanArgs a, int B, cudaStream_t st) {
-    using Gm = ScanGeom<NS, 2, kBwdL>;
-    constexpr size_t kRun = kScanWarps * (6 * Gm::L * Gm::CPW + 2 * Gm::L * Gm::NP + Gm::QUADS) * sizeof(float);
-    constexpr size_t kRed = kScanWarps * (Gm::QUADS + 2 * Gm::CPW) * sizeof(float);
-    constexpr size_t smem = kRun > kRed ? kRun : kRed;
-    auto kern = scan_bwd_kernel<T, TG, Gm>;
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    kern<<<(unsigned)((long long)B * a.G * a.tiles), kScanThreads, smem, st>>>(a);
+template <typename T, typename TG, int NS, bool ENDS>
+static cudaError_t launch_bwd_geom(const ScanArgs& a, int B, cudaStream_t st) {
+    using Gm = ScanGeom<NS>;
+    constexpr size_t smem = ScanBwdShared<Gm>::total * sizeof(float);
+    static_assert(smem <= 227 * 1024, "shared memory of a block");
+    auto kern = scan_bwd_kernel<T, TG, Gm, ENDS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)((long long)B * a.G * a.tiles * a.chunks), kScanThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T, typename TG> static cudaError_t launch_bwd_lanes(const ScanArgs& a, int B, cudaStream_t st) {
+template <typename T, typename TG, bool ENDS> static cudaError_t launch_bwd_lanes(const ScanArgs& a, int B, cudaStream_t st) {
     switch (scan_lanes(a.N)) {
-        case 1: return launch_bwd_geom<T, TG, 1>(a, B, st);
-        case 2: return launch_bwd_geom<T, TG, 2>(a, B, st);
-        case 4: return launch_bwd_geom<T, TG, 4>(a, B, st);
-        case 8: return launch_bwd_geom<T, TG, 8>(a, B, st);
-        case 16: return launch_bwd_geom<T, TG, 16>(a, B, st);
-        default: return launch_bwd_geom<T, TG, 32>(a, B, st);
+        case 1: return launch_bwd_geom<T, TG, 1, ENDS>(a, B, st);
+        case 2: return launch_bwd_geom<T, TG, 2, ENDS>(a, B, st);
+        case 4: return launch_bwd_geom<T, TG, 4, ENDS>(a, B, st);
+        case 8: return launch_bwd_geom<T, TG, 8, ENDS>(a, B, st);
+        case 16: return launch_bwd_geom<T, TG, 16, ENDS>(a, B, st);
+        default: return launch_bwd_geom<T, TG, 32, ENDS>(a, B, st);
     }
+}
+template <bool ENDS>
+static cudaError_t launch_bwd_types(const ScanArgs& a, int B, int dtype, int grad_dtype, cudaStream_t st) {
+    return dtype == GDR_FP32        ? launch_bwd_lanes<float, float, ENDS>(a, B, st)
+           : grad_dtype == GDR_FP32 ? launch_bwd_lanes<__nv_bfloat16, float, ENDS>(a, B, st)
+                                    : launch_bwd_lanes<__nv_bfloat16, __nv_bfloat16, ENDS>(a, B, st);
 }
 
 cudaError_t launch_scan_bwd(ScanArgs a, void* ws, float* dA, float* dB, float* dC, float* dD, float* dbias, int B,
                             int dtype, int grad_dtype, cudaStream_t st) {
-    const ScanBwdLayout l = scan_bwd_layout(B, a.T, a.D_, a.N, a.G);
+    const int chunks = scan_bwd_chunks(B, a.T, a.K, a.N, a.G);
+    const ScanBwdLayout l = scan_bwd_layout(B, a.T, a.D_, a.N, a.G, chunks);
     char* w = reinterpret_cast<char*>(ws);
     a.ckpt = reinterpret_cast<float*>(w + l.ckpt);
     a.bcpart = reinterpret_cast<float*>(w + l.bc);
     a.prm = reinterpret_cast<float*>(w + l.prm);
-    a.nseg = (a.T + kBwdL - 1) / kBwdL;
-    a.tiles = bwd_tiles(a.K, a.N);
-    if ((long long)B * a.G * a.tiles > 0x7fffffffll) return cudaErrorInvalidValue;
-    cudaError_t e = a.T > 0 ? launch_scan_ckpt(a, B, dtype, st) : cudaSuccess;
+    a.ends = reinterpret_cast<float*>(w + l.ends);
+    a.grad_ends = reinterpret_cast<float*>(w + l.grad_ends);
+    a.segs = bwd_segments(a.T, a.N);
+    scan_split(a, chunks);
+    if ((long long)B * a.G * a.tiles * a.chunks > 0x7fffffffll) return cudaErrorInvalidValue;
+    cudaError_t e = a.chunks > 1 ? launch_bwd_types<true>(a, B, dtype, grad_dtype, st) : cudaSuccess;
     if (e != cudaSuccess) return e;
-    e = dtype == GDR_FP32 ? launch_bwd_lanes<float, float>(a, B, st)
-        : grad_dtype == GDR_FP32 ? launch_bwd_lanes<__nv_bfloat16, float>(a, B, st)
-                                 : launch_bwd_lanes<__nv_bfloat16, __nv_bfloat16>(a, B, st);
+    e = a.T > 0 ? launch_scan_ckpt(a, B, dtype, st) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    e = launch_bwd_types<false>(a, B, dtype, grad_dtype, st);
     if (e != cudaSuccess) return e;
     ScanReduce r = {};
     r.bcpart = a.bcpart; r.prm = a.prm; r.lengths = a.lengths;
     r.dB = dB; r.dC = dC; r.dA = dA; r.dD = dD; r.dbias = dbias;
     r.vecs = (long long)B * a.T * a.G;
-    r.B = B; r.T = a.T; r.G = a.G; r.D_ = a.D_; r.N = a.N; r.NP = 4 * scan_lanes(a.N); r.tiles = a.tiles;
+    r.T = a.T; r.G = a.G; r.D_ = a.D_; r.N = a.N; r.NP = 4 * scan_lanes(a.N); r.tiles = a.tiles;
+    r.parts = B * a.chunks;
     const long long bc = (r.vecs * 2 * r.NP + 255) / 256, pr = ((long long)a.D_ * (a.N + 2) + 255) / 256;
     if (bc + pr > 0x7fffffffll) return cudaErrorInvalidValue;
     r.bc_blocks = (unsigned)bc;

@@ -1,5 +1,5 @@
-// Selective state-space scan: geometry, staging and pair arithmetic shared by
-// the forward and backward kernels.
+// Selective state-space scan: geometry, staging and exchange shared by the
+// forward and backward kernels.
 //
 // Per channel d and state entry n, with dt = softplus(delta + bias) (or
 // delta + bias):
@@ -7,21 +7,25 @@
 //   y_t = sum_n C_t[n] h_t + D[d] u_t,   out_t = y_t z_t sigmoid(z_t)  (or y_t)
 // Channel d of group g reads B[g], C[g]; K = D / G channels share a group.
 //
-// Geometry. A warp holds CPW channels of one (sequence, group) with all their
-// states: a lane owns 4 adjacent states of CH channels, NS lanes cover the
-// states (4 NS >= N, the rest padded with A = B = C = 0) and 32 / NS lanes the
-// channels. A block of kScanWarps warps holds one such channel tile; its warps
-// take segments of L tokens in turn. What is serial, the state passed from a
-// segment to the next, is one multiply-add per state and segment: a warp first
-// works through its segment from a zero state while it waits.
+// Geometry. Two kinds of warps share a block, one of each on every scheduler.
+// Four walkers hold a tile of CPW channels each with all their states: a lane
+// owns 4 adjacent states of 2 channels, NS lanes cover the states (4 NS >= N,
+// the rest padded with A = B = C = 0) and 32 / NS lanes the channels. Four
+// helpers turn the inputs of the block's CB = 4 CPW channels into what a walker
+// reads per token (dt, dt u; B and C once for the block), LT tokens ahead of
+// them, and its sums into outputs, LT tokens behind; one barrier per LT tokens.
+// So a walker's stream is the recurrence alone, and the softplus, gates,
+// conversions and global accesses fill the issue slots between its exponentials.
+// (All of it in one warp, with segments of 8 tokens per warp and their states
+// joined by a barrier per 64 tokens, ran at 0.47 instructions per cycle: 856 us
+// for 4 x 4096 tokens x 4096 channels x 16 states.)
 #pragma once
 
 #include "layer_common.cuh"
 
 namespace gdr {
 
-constexpr int kScanWarps = 8;
-constexpr int kScanThreads = 32 * kScanWarps;
+constexpr int kWalkers = 4, kHelperThreads = 128, kScanThreads = 32 * kWalkers + kHelperThreads;
 
 __device__ __forceinline__ void lds_quad(f2 (&q)[2], const float* p) {
     const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
@@ -32,18 +36,6 @@ __device__ __forceinline__ void sts_quad(float* p, const f2 (&q)[2]) {
     *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(q[0], q[1]);
 }
 
-// CH adjacent floats of shared memory.
-template <int CH> __device__ __forceinline__ void lds_run(float (&f)[CH], const float* p) {
-    static_assert(CH == 2 || CH == 4, "channels of a lane");
-    if constexpr (CH == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-    } else {
-        const float2 v = *reinterpret_cast<const float2*>(p);
-        f[0] = v.x; f[1] = v.y;
-    }
-}
-
 // ---- arguments ----
 struct ScanArgs {
     const void *u, *delta, *Bm, *Cm, *z, *dy;
@@ -52,49 +44,68 @@ struct ScanArgs {
     void* y;
     float* h_T;
     long long us[2], ds[2], bs[2], cs[2], zs[2], gs[2];  // batch and token strides
-    int T, D_, N, G, K, tiles, softplus, state_vec, bc_vec;
+    int T, D_, N, G, K, tiles, softplus;
+    int state_vec, bc_vec, act_vec;  // wide accesses: states, B and C, token rows
     // backward
     const float* dh_T;
     float *du, *ddelta, *dz, *dh0;
-    float* ckpt;    // state at every segment's start, lane order
-    float* bcpart;  // dB, dC of each channel tile
-    float* prm;     // dA, dD, ddelta_bias of each sequence
-    int nseg;       // segments of T tokens
+    float* ckpt;    // state every Seg tokens, lane order
+    float* bcpart;  // dB, dC of each block's channels
+    float* prm;     // dA, dD, ddelta_bias of each sequence and chunk
+    int segs;       // segments of T tokens
+    // time split: chunks of `chunk` tokens, `chunks` of them; maps of each (decay, end)
+    int chunk, chunks;
+    float *ends, *grad_ends;
 };
 
-template <int NS_, int CH_, int L_> struct ScanGeom {
-    static constexpr int NS = NS_, CH = CH_, L = L_;
-    static constexpr int NP = 4 * NS;          // padded states
-    static constexpr int CL = 32 / NS;         // channel lanes
-    static constexpr int CPW = CH * CL;        // channels of a warp (and block)
-    static constexpr int SE = (L * CPW + 31) / 32;  // staged token-channels per lane
-    static constexpr int BE = (L * NP + 31) / 32;   // staged B (or C) values per lane
-    static constexpr int QUADS = CH * 32 * 4;  // floats of a warp's state
+template <int NS_> struct ScanGeom {
+    static constexpr int NS = NS_, CH = 2;
+    static constexpr int NP = 4 * NS;               // padded states
+    static constexpr int CL = 32 / NS;              // channel lanes
+    static constexpr int CPW = CH * CL;             // channels of a walker
+    static constexpr int CB = kWalkers * CPW;       // channels of a block
+    static constexpr int NQ = NS < 4 ? NS : 4;      // partial sums over the states that go to shared memory
+    static constexpr int QUADS = CH * 32 * 4;       // floats of a walker's state
+    static constexpr int LT = NS >= 4 ? 16 : NS == 2 ? 8 : 4;  // tokens of a step: bounded by shared memory
+    static constexpr int Seg = NS == 1 ? 4 : 8;     // tokens of a backward segment
+    static constexpr int VPT = CB / 4;              // vectors of 4 channels of a token
 };
 
-// Block -> (sequence, group, channel tile), tile fastest: blocks that share
-// B and C run together.
+// Vectors of 4 elements that one of the helper threads holds of L token rows.
+template <typename Gm, int L> constexpr int row_vecs() { return L * Gm::VPT > kHelperThreads ? L * Gm::VPT / kHelperThreads : 1; }
+template <typename Gm, int L> constexpr int state_vecs() { return 2 * L * Gm::NS > kHelperThreads ? 2 * L * Gm::NS / kHelperThreads : 1; }
+
+// Block -> (sequence, group, channel tile, chunk of tokens), tile fastest:
+// blocks that share B and C run together. Tokens [t0, n) are this chunk's,
+// rows [t0, t1) its outputs'.
 struct ScanTile {
-    int b, g, tile, c0, kleft, n;
-    __device__ __forceinline__ ScanTile(const ScanArgs& a, int cpw) {
-        const int blk = blockIdx.x;
-        tile = blk % a.tiles;
-        const int r = blk / a.tiles;
-        g = r % a.G;
-        b = r / a.G;
-        c0 = g * a.K + tile * cpw;
-        kleft = min(cpw, a.K - tile * cpw);
-        n = seq_len(a.lengths, b, a.T);
+    int b, g, tile, part, c0, kleft, t0, t1, n;
+    size_t unit;  // of (sequence, group, tile)
+    __device__ __forceinline__ ScanTile(const ScanArgs& a, int cb) {
+        unsigned blk = blockIdx.x;
+        tile = blk % (unsigned)a.tiles;
+        blk /= (unsigned)a.tiles;
+        part = blk % (unsigned)a.chunks;
+        blk /= (unsigned)a.chunks;
+        g = blk % (unsigned)a.G;
+        b = blk / (unsigned)a.G;
+        unit = ((size_t)b * a.G + g) * a.tiles + tile;
+        c0 = g * a.K + tile * cb;
+        kleft = min(cb, a.K - tile * cb);
+        t0 = part * a.chunk;
+        t1 = min(a.T, t0 + a.chunk);
+        n = max(t0, min(t1, seq_len(a.lengths, b, a.T)));
     }
 };
 
-// One lane's states of the tile's channels, [D, N] (A) or [B, D, N] layout.
+// One lane's states of its channels (ch0 of the block's on), [D, N] (A) or
+// [B, D, N] layout.
 template <typename Gm>
 __device__ __forceinline__ void load_states(f2 (&s)[Gm::CH][2], const float* p, const ScanTile& tl, int N, int vec,
-                                            int cl, int nl, float scale, bool clamp) {
+                                            int ch0, int nl, float scale, bool clamp) {
 #pragma unroll
     for (int c = 0; c < Gm::CH; ++c) {
-        const int ch = cl * Gm::CH + c;
+        const int ch = ch0 + c;
         float f[4] = {0.f, 0.f, 0.f, 0.f};
         if (ch < tl.kleft && nl * 4 < N) {
             const float* q = p + (size_t)(tl.c0 + ch) * N + nl * 4;
@@ -115,109 +126,180 @@ __device__ __forceinline__ void load_states(f2 (&s)[Gm::CH][2], const float* p, 
         s[c][1] = pack2(f[2], f[3]);
     }
 }
+// The state a sequence starts (or a gradient ends) with: p's, or 0 without p.
 template <typename Gm>
-__device__ __forceinline__ void store_states(float* p, const f2 (&s)[Gm::CH][2], const ScanTile& tl, int N, int vec,
-                                             int cl, int nl) {
+__device__ __forceinline__ void load_given(f2 (&s)[Gm::CH][2], const float* p, const ScanArgs& a, const ScanTile& tl,
+                                           int ch0, int nl) {
+    if (p) {
+        load_states<Gm>(s, p + (size_t)tl.b * a.D_ * a.N, tl, a.N, a.state_vec, ch0, nl, 1.f, false);
+    } else {
+#pragma unroll
+        for (int c = 0; c < Gm::CH; ++c) s[c][0] = s[c][1] = both2(0.f);
+    }
+}
+template <typename Gm>
+__device__ __forceinline__ void store_states(float* p, const f2 (&s)[Gm::CH][2], const ScanArgs& a, const ScanTile& tl,
+                                             int ch0, int nl) {
 #pragma unroll
     for (int c = 0; c < Gm::CH; ++c) {
-        const int ch = cl * Gm::CH + c;
-        if (ch >= tl.kleft || nl * 4 >= N) continue;
+        const int ch = ch0 + c;
+        if (ch >= tl.kleft || nl * 4 >= a.N) continue;
         float f[4];
         unpack2(s[c][0], f[0], f[1]);
         unpack2(s[c][1], f[2], f[3]);
-        float* q = p + (size_t)(tl.c0 + ch) * N + nl * 4;
-        if (vec) VecIO<float, 4>::store(q, f);
+        float* q = p + ((size_t)tl.b * a.D_ + tl.c0 + ch) * a.N + nl * 4;
+        if (a.state_vec) VecIO<float, 4>::store(q, f);
         else
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (nl * 4 + i < N) q[i] = f[i];
+                if (nl * 4 + i < a.N) q[i] = f[i];
     }
 }
 
-// A tile's [L tokens][CPW channels] of one input, as the lanes stage it:
-// element i of a lane is token (32 i + lane) / CPW, channel (32 i + lane) % CPW.
-// Tokens from n on and channels beyond the tile are not read and give 0.
-template <typename T, typename Gm>
-__device__ __forceinline__ void fetch_rows(T (&r)[Gm::SE], const T* p, long long st, int t0, const ScanTile& tl,
-                                           int lane) {
+// [L tokens][CB channels] of one input among the helpers: vector i of thread
+// `ht` is number v = 128 i + ht, token v / VPT, channels from (v % VPT) 4 (the
+// same for every i). Tokens from n on and channels beyond the tile are not read
+// and give 0.
+template <typename T, typename Gm, int L> struct TokenRows {
+    static constexpr int NV = row_vecs<Gm, L>();
+    RawVec<T, 4> v[NV];
+    static __device__ __forceinline__ int token(int i, int ht) { return (kHelperThreads * i + ht) / Gm::VPT; }
+    __device__ __forceinline__ void fetch(const T* p, long long st, int t0, const ScanTile& tl, int vec, int ht) {
+        const int ch = ht % Gm::VPT * 4;
 #pragma unroll
-    for (int i = 0; i < Gm::SE; ++i) {
-        const int e = 32 * i + lane, step = e / Gm::CPW, ch = e % Gm::CPW;
-        r[i] = from_f32<T>(0.f);
-        if (step < Gm::L && t0 + step < tl.n && ch < tl.kleft) r[i] = p[(t0 + step) * st + ch];
-    }
-}
-template <typename T, typename Gm>
-__device__ __forceinline__ void fetch_vecs(T (&r)[Gm::BE], const T* p, long long st, int t0, const ScanTile& tl, int N,
-                                           int lane) {
+        for (int i = 0; i < NV; ++i) {
+            const int tok = token(i, ht);
+            v[i].zero();
+            if (tok >= L || t0 + tok >= tl.n || ch >= tl.kleft) continue;
+            const T* q = p + (t0 + tok) * st + ch;
+            if (vec) v[i].load(q);
+            else
 #pragma unroll
-    for (int i = 0; i < Gm::BE; ++i) {
-        const int e = 32 * i + lane, step = e / Gm::NP, n = e % Gm::NP;
-        r[i] = from_f32<T>(0.f);
-        if (step < Gm::L && t0 + step < tl.n && n < N) r[i] = p[(t0 + step) * st + n];
-    }
-}
-template <typename T, typename Gm>
-__device__ __forceinline__ void stage_vecs(float* s, const T (&r)[Gm::BE], int lane) {
-#pragma unroll
-    for (int i = 0; i < Gm::BE; ++i) {
-        const int e = 32 * i + lane;
-        if (e < Gm::L * Gm::NP) s[e] = to_f32(r[i]);
-    }
-}
-
-// Named barriers 1..kScanWarps hand a warp its incoming state: the producer
-// arrives without waiting, the consumer waits. Used once per segment; a
-// producer's next arrival follows, through the chain of segments, the
-// consumer's last wait, so the barrier never sees two arrivals in a row.
-__device__ __forceinline__ void carry_arrive(int warp) {
-    __syncwarp();
-    __threadfence_block();
-    asm volatile("bar.arrive %0, 64;" ::"r"(warp + 1) : "memory");
-}
-__device__ __forceinline__ void carry_wait(int warp) {
-    __syncwarp();
-    asm volatile("bar.sync %0, 64;" ::"r"(warp + 1) : "memory");
-}
-
-// Sums V values of each lane over the 2^k lanes whose numbers differ in the
-// bits STRIDE .. STRIDE * LANES / 2. While V is even a step halves the values
-// a lane keeps (one shuffle per value kept); the lane's bit of that step says
-// which half it holds. Returns the number of values left.
-template <int V, int LANES, int STRIDE> struct LaneSum {
-    static constexpr int left() {
-        if constexpr (LANES > 1 && V % 2 == 0) return LaneSum<V / 2, LANES / 2, STRIDE * 2>::left();
-        else return V;
-    }
-    template <int VV> static __device__ __forceinline__ void run(float (&v)[VV], int lane) {
-        if constexpr (LANES > 1 && V % 2 == 0) {
-            const bool up = lane & STRIDE;
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                const float keep = up ? v[V / 2 + i] : v[i], give = up ? v[i] : v[V / 2 + i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, STRIDE);
-            }
-            LaneSum<V / 2, LANES / 2, STRIDE * 2>::run(v, lane);
-        } else if constexpr (LANES > 1) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], STRIDE);
-            LaneSum<V, LANES / 2, STRIDE * 2>::run(v, lane);
+                for (int j = 0; j < 4; ++j)
+                    if (ch + j < tl.kleft) v[i].set(j, q[j]);
         }
     }
-    // index of value 0 held by this lane among the original V, and whether it
-    // is the one lane of its copies that writes
-    static __device__ __forceinline__ int first(int lane) {
-        if constexpr (LANES > 1 && V % 2 == 0)
-            return ((lane & STRIDE) ? V / 2 : 0) + LaneSum<V / 2, LANES / 2, STRIDE * 2>::first(lane);
-        else if constexpr (LANES > 1) return LaneSum<V, LANES / 2, STRIDE * 2>::first(lane);
-        else return 0;
+};
+template <typename T, bool VEC4>
+__device__ __forceinline__ void store_row(T* p, const float (&f)[4], int left) {
+    if constexpr (VEC4) VecIO<T, 4>::store(p, f);
+    else
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < left) p[j] = from_f32<T>(f[j]);
+}
+template <typename T> __device__ __forceinline__ void store_row(T* p, const float (&f)[4], int left, int vec) {
+    if (vec) store_row<T, true>(p, f, left);
+    else store_row<T, false>(p, f, left);
+}
+
+// [L tokens][N states] of B and of C behind it, staged as fp32 rows of NP.
+template <typename T, typename Gm, int L> struct StateRows {
+    static constexpr int NV = state_vecs<Gm, L>(), kEach = L * Gm::NS;
+    RawVec<T, 4> v[NV];
+    __device__ __forceinline__ void fetch(const T* Bp, const T* Cp, const ScanArgs& a, int t0, const ScanTile& tl,
+                                          int ht) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = kHelperThreads * i + ht, r = e % kEach, tok = r / Gm::NS, n0 = r % Gm::NS * 4;
+            const T* p = e < kEach ? Bp : Cp;
+            v[i].zero();
+            if (e >= 2 * kEach || !p || t0 + tok >= tl.n || n0 >= a.N) continue;
+            const T* q = p + (t0 + tok) * (e < kEach ? a.bs[1] : a.cs[1]) + n0;
+            if (a.bc_vec) v[i].load(q);
+            else
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n0 + j < a.N) v[i].set(j, q[j]);
+        }
     }
-    static __device__ __forceinline__ bool owner(int lane) {
-        if constexpr (LANES > 1 && V % 2 == 0) return LaneSum<V / 2, LANES / 2, STRIDE * 2>::owner(lane);
-        else if constexpr (LANES > 1) return !(lane & STRIDE) && LaneSum<V, LANES / 2, STRIDE * 2>::owner(lane);
-        else return true;
+    __device__ __forceinline__ void stage(float* s, int ht) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = kHelperThreads * i + ht;
+            if (e >= 2 * kEach) continue;
+            const f2 q[2] = {pack2(v[i].get(0), v[i].get(1)), pack2(v[i].get(2), v[i].get(3))};
+            sts_quad(s + 4 * e, q);
+        }
     }
 };
+
+template <typename T> __device__ __forceinline__ void raw_floats(float (&f)[4], const RawVec<T, 4>& r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = r.get(i);
+}
+// dt of 4 raw steps.
+__device__ __forceinline__ void step_sizes(float (&dt)[4], const float (&raw)[4], int softplus) {
+    if (softplus) {
+        unpack2(softplus2(pack2(raw[0], raw[1])), dt[0], dt[1]);
+        unpack2(softplus2(pack2(raw[2], raw[3])), dt[2], dt[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dt[i] = raw[i];
+    }
+}
+// Four channels' values from a [D] array, 0 where absent.
+__device__ __forceinline__ void channel_values(float (&f)[4], const float* p, const ScanTile& tl, int ch) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = p && ch + j < tl.kleft ? p[tl.c0 + ch + j] : 0.f;
+}
+
+// Place of a block's channel among the values of one token, in the order the
+// walkers' lanes read them: walker, channel of the lane, lane.
+template <typename Gm> __device__ __forceinline__ int channel_place(int ch) {
+    const int in = ch % Gm::CPW;
+    return (ch / Gm::CPW * Gm::CH + in % Gm::CH) * Gm::CL + in / Gm::CH;
+}
+template <typename Gm> __device__ __forceinline__ int lane_place(int walker, int c, int cl) {
+    return (walker * Gm::CH + c) * Gm::CL + cl;
+}
+
+// Partial sums over the states: lanes whose numbers differ in bits above the
+// lowest two are added here, the rest (NQ per channel, adjacent) by the reader.
+template <typename Gm> __device__ __forceinline__ float fold_states(float v) {
+#pragma unroll
+    for (int m = 4; m < Gm::NS; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
+template <typename Gm> __device__ __forceinline__ float sum_states(const float* p) {
+    if constexpr (Gm::NQ == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        return (v.x + v.y) + (v.z + v.w);
+    } else if constexpr (Gm::NQ == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        return v.x + v.y;
+    } else {
+        return p[0];
+    }
+}
+
+// Folds the maps state -> P state + h of the chunks [from, to) (step 1 or -1) of
+// a walker's channels into s. Maps: [unit][chunk][walker][P, h].
+template <typename Gm>
+__device__ __forceinline__ void fold_chunks(f2 (&s)[Gm::CH][2], const float* ends, const ScanArgs& a,
+                                            const ScanTile& tl, int walker, int lane, int from, int to, int step) {
+    for (int c = from; c != to; c += step) {
+        const float* p = ends + ((tl.unit * a.chunks + c) * kWalkers + walker) * 2 * Gm::QUADS + lane * 4;
+#pragma unroll
+        for (int i = 0; i < Gm::CH; ++i) {
+            f2 pw[2], hw[2];
+            lds_quad(pw, p + i * 128);
+            lds_quad(hw, p + Gm::QUADS + i * 128);
+            s[i][0] = fma2(pw[0], s[i][0], hw[0]);
+            s[i][1] = fma2(pw[1], s[i][1], hw[1]);
+        }
+    }
+}
+template <typename Gm>
+__device__ __forceinline__ void store_map(float* ends, const f2 (&p)[Gm::CH][2], const f2 (&h)[Gm::CH][2],
+                                          const ScanArgs& a, const ScanTile& tl, int walker, int lane) {
+    float* o = ends + ((tl.unit * a.chunks + tl.part) * kWalkers + walker) * 2 * Gm::QUADS + lane * 4;
+#pragma unroll
+    for (int i = 0; i < Gm::CH; ++i) {
+        sts_quad(o + i * 128, p[i]);
+        sts_quad(o + Gm::QUADS + i * 128, h[i]);
+    }
+}
 
 // Lanes that share a channel's states, by the state size.
 inline int scan_lanes(int N) {
@@ -225,5 +307,6 @@ inline int scan_lanes(int N) {
     while (4 * ns < N) ns *= 2;
     return ns;
 }
+inline int scan_tiles(int K, int N) { const int cb = kWalkers * 64 / scan_lanes(N); return (K + cb - 1) / cb; }
 
 }  // namespace gdr

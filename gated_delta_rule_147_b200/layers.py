@@ -249,12 +249,14 @@ def _scan_strides(u, delta, Bm, Cm, z, lead, Dn, N, G, dev, n):
 
 
 def scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, h0=None, *, delta_bias=None, delta_softplus=False,
-             lengths=None, out=None, final_state=True, h_T=None, stream=None):
+             lengths=None, workspace="auto", out=None, final_state=True, h_T=None, stream=None):
     """Selective scan over [B, T, D] inputs u and step sizes delta (delta_bias
     [D] added, then softplus with delta_softplus): A [D, N] and D [D] float32,
     Bm, Cm [B, T, G, N] shared by the D / G channels of a group, z [B, T, D] a
     gate (y z sigmoid(z)), h0 [B, D, N] float32 (None: zeros). Returns (y, h_T),
-    h_T None when final_state is False; h_T may be h0."""
+    h_T None when final_state is False; h_T may be h0. workspace: "auto" takes
+    from torch what a split of the tokens needs (few channels, many tokens), a
+    device tensor supplies it, None leaves the tokens unsplit."""
     code, dev = _first("u", u, 3)
     lead = tuple(u.shape[:2])
     B, T = lead
@@ -274,7 +276,16 @@ def scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, h0=None, *, delta_bias=None, d
         h_T = None
     elif h_T is None:
         h_T = at.empty((B, Dn, N), torch.float32)
-    at.run(_lib.gdr_scan_fwd, u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, y, h_T, _i64(*st), B, T, Dn, N, G,
+    ws, nbytes = None, 0
+    if workspace is not None:
+        nbytes = _lib.gdr_scan_fwd_workspace_size(B, T, Dn, N, G)
+        if isinstance(workspace, str):
+            if workspace != "auto":
+                raise ValueError(workspace)
+            workspace = None
+        if nbytes:
+            ws, nbytes = at.scratch(workspace, nbytes)
+    at.run(_lib.gdr_scan_fwd, u, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, y, h_T, ws, nbytes, _i64(*st), B, T, Dn, N, G,
            int(bool(delta_softplus)), code)
     return y, h_T
 

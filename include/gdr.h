@@ -463,12 +463,17 @@ gdr_status gdr_conv_step(const void* x, const void* weight, const void* bias, vo
  * [D_] or NULL, z NULL for no gate; h0, h_T [B, D_, N] fp32 or NULL (h0 = 0 /
  * not written), h_T may be h0; y [B, T, D_]. strides: batch and token of u,
  * delta, Bm, Cm, z. 1 <= N <= 128, D_ a multiple of G.
+ * workspace: NULL, or gdr_scan_fwd_workspace_size() bytes, 256-byte aligned;
+ * with it the tokens are split where there are few channels (a size of 0 says
+ * that they are not; a smaller workspace is not used). Contents on entry
+ * ignored, on exit undefined. A split call's results differ in rounding.
  */
 gdr_status gdr_scan_fwd(const void* u, const void* delta, const float* A, const void* Bm,
                         const void* Cm, const float* D, const void* z, const float* delta_bias,
                         const float* h0, const int* lengths, void* y, float* h_T,
-                        const long long* strides, int B, int T, int D_, int N, int G,
-                        int delta_softplus, int dtype, void* stream);
+                        void* workspace, size_t workspace_bytes, const long long* strides, int B,
+                        int T, int D_, int N, int G, int delta_softplus, int dtype, void* stream);
+size_t gdr_scan_fwd_workspace_size(int B, int T, int D_, int N, int G);
 
 /*
  * gdr_scan_bwd -- gradients of gdr_scan_fwd given dy [B, T, D_] (grad_dtype)
@@ -477,8 +482,8 @@ gdr_status gdr_scan_fwd(const void* u, const void* delta, const float* A, const 
  * and ddelta_bias are NULL exactly when z, D and delta_bias are; dh0 may be
  * NULL and needs h0. strides: as gdr_scan_fwd, then dy batch, token.
  * workspace: at least gdr_scan_bwd_workspace_size() bytes, 256-byte aligned
- * (the state every 8 tokens, sums of dB and dC per channel tile, sums of the
- * parameter gradients per sequence).
+ * (the state every 8 tokens, sums of dB and dC per 64 channels of 16 states, sums
+ * of the parameter gradients per sequence).
  */
 gdr_status gdr_scan_bwd(const void* u, const void* delta, const float* A, const void* Bm,
                         const void* Cm, const float* D, const void* z, const float* delta_bias,

@@ -140,6 +140,9 @@ SCAN = [  # dtype, B, T, D, N, G, softplus, gate, skip, bias, state, lengths, sl
     (BF, 2, 40, 16, 24, 4, False, True, True, True, False, False, 8),
     (F32, 2, 0, 8, 8, 1, True, True, True, True, True, False, 4),
     (F32, 1, 700, 3, 8, 1, True, False, True, True, True, False, 1),
+    (BF, 1, 1043, 40, 16, 1, True, True, True, True, True, False, 8),
+    (F32, 3, 800, 9, 6, 1, True, True, True, True, True, True, 1),
+    (BF, 2, 50, 300, 4, 1, True, True, True, True, True, False, 8),
 ]
 
 
@@ -184,6 +187,22 @@ def test_scan(cuda_device, dtype, B, T, D, N, G, softplus, gate, skip, bias, sta
     g = gdr.scan_bwd(*args, dy=dy, need_dh0=False, **kw)
     assert g["dh0"] is None
     check_scan(g, ref, ("du", "ddelta", "dA", "dB", "dC"))
+
+
+def test_scan_split_workspace(cuda_device):
+    """The split of the tokens needs a workspace; without one, or with one too
+    small, the call runs unsplit, with the same results up to rounding."""
+    r = Rnd(cuda_device, 77)
+    B, T, D, N = 1, 1500, 24, 16
+    i = scan_inputs(r, F32, B, T, D, N, 1, True, True, True, True, True)
+    args = tuple(i[k] for k in ("u", "delta", "A", "Bm", "Cm", "D", "z", "h0"))
+    kw = dict(delta_bias=i["delta_bias"], delta_softplus=True)
+    ref = R.scan(*args, i["delta_bias"], True)
+    got = {}
+    for name, ws in (("auto", "auto"), ("none", None), ("small", torch.empty(256, dtype=torch.uint8, device=cuda_device))):
+        got[name] = gdr.scan_fwd(*args, workspace=ws, **kw)
+        check_scan(dict(zip(("y", "h_T"), got[name])), ref, ("y", "h_T"))
+    assert torch.equal(got["none"][0], got["small"][0]) and torch.equal(got["none"][1], got["small"][1])
 
 
 @pytest.mark.parametrize("dtype,D,N,G", [(BF, 48, 16, 1), (F32, 10, 7, 2), (BF, 4, 128, 1), (F32, 33, 4, 1)])
