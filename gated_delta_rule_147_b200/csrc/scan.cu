@@ -45,6 +45,16 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a) {
                 const float* in = sm + (s & 1) * kIn + lane_place<Gm>(warp, 0, cl) * 4;
                 const float* B0 = sm + (s & 1) * kIn + 4 * LT * CB + 4 * nl;
                 float* o = out + (s & 1) * kOut + lane_place<Gm>(warp, 0, cl) * Gm::NQ + nl;
+                // a token's operands are loaded before the last one's sums are stored:
+                // the compiler cannot tell that the two do not overlap
+                struct { f2 B[2], C[2], d[CH][2]; } x, next;  // d: dt, dt u
+                auto load = [&](decltype(x)& v, int t) {
+                    lds_quad(v.B, B0 + t * NP);
+                    if (MODE == kScanOut) lds_quad(v.C, B0 + (LT + t) * NP);
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) lds_quad(v.d[c], in + (t * CB + c * CL) * 4);
+                };
+                load(x, 0);
 #pragma unroll 1
                 for (int tb = 0; tb < LT; tb += Gm::Seg) {
                     if (MODE == kScanCkpt) {
@@ -57,22 +67,19 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a) {
 #pragma unroll
                     for (int i = 0; i < Gm::Seg; ++i) {
                         const int t = tb + i;
-                        f2 B[2], C[2];
-                        lds_quad(B, B0 + t * NP);
-                        if (MODE == kScanOut) lds_quad(C, B0 + (LT + t) * NP);
+                        load(next, min(t + 1, LT - 1));
 #pragma unroll
                         for (int c = 0; c < CH; ++c) {
-                            f2 d[2];  // dt, dt u
-                            lds_quad(d, in + (t * CB + c * CL) * 4);
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
-                                h[c][k] = fma2(ex2_pair(mul2(d[0], A[c][k])), h[c][k], mul2(d[1], B[k]));
-                            if (MODE == kScanEnds) total[c] = add2(total[c], d[0]);
+                                h[c][k] = fma2(ex2_pair(mul2(x.d[c][0], A[c][k])), h[c][k], mul2(x.d[c][1], x.B[k]));
+                            if (MODE == kScanEnds) total[c] = add2(total[c], x.d[c][0]);
                             if (MODE == kScanOut) {
-                                const float v = fold_states<Gm>(sum2(fma2(C[1], h[c][1], mul2(C[0], h[c][0]))));
+                                const float v = fold_states<Gm>(sum2(fma2(x.C[1], h[c][1], mul2(x.C[0], h[c][0]))));
                                 if (nl < Gm::NQ) o[(t * CB + c * CL) * Gm::NQ] = v;
                             }
                         }
+                        x = next;
                     }
                 }
             }

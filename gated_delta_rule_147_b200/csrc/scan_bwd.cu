@@ -130,39 +130,56 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
                             }
                         }
                     }
-#pragma unroll
-                    for (int t = L - 1; t >= 0; --t) {
-                        f2 B[2], C[2], dB[2], dC[2];
-                        lds_quad(B, in + Sh::B + t * NP + 4 * nl);
-                        lds_quad(C, in + Sh::B + (L + t) * NP + 4 * nl);
+                    // a token's operands are loaded before the last one's sums are
+                    // stored: the compiler cannot tell that the two do not overlap
+                    struct { f2 B[2], C[2], d[CH][2], dyh[CH]; } x, next;  // d: dt, dt u
+                    auto load = [&](decltype(x)& v, int t) {
+                        lds_quad(v.B, in + Sh::B + t * NP + 4 * nl);
+                        lds_quad(v.C, in + Sh::B + (L + t) * NP + 4 * nl);
 #pragma unroll
                         for (int c = 0; c < CH; ++c) {
                             const int at = t * CB + c * CL + at0;
-                            f2 d[2], yc, gB, dd;
-                            lds_quad(d, in + at * 4);
-                            const f2 dyh = *reinterpret_cast<const f2*>(in + Sh::dy + at * 2);
+                            lds_quad(v.d[c], in + at * 4);
+                            v.dyh[c] = *reinterpret_cast<const f2*>(in + Sh::dy + at * 2);
+                        }
+                    };
+                    load(x, L - 1);
+#pragma unroll
+                    for (int t = L - 1; t >= 0; --t) {
+                        if (t > 0) load(next, t - 1);
+                        f2 dB[2], dC[2];
+                        float vy[CH], vg[CH], vd[CH];
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            f2 yc, gB, dd;
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const f2 gt = fma2(C[k], dyh, g[c][k]), ht = h[t][c][k];
-                                yc = k == 0 ? mul2(C[k], ht) : fma2(C[k], ht, yc);
-                                gB = k == 0 ? mul2(B[k], gt) : fma2(B[k], gt, gB);
-                                dB[k] = c == 0 ? mul2(gt, d[1]) : fma2(gt, d[1], dB[k]);
-                                dC[k] = c == 0 ? mul2(ht, dyh) : fma2(ht, dyh, dC[k]);
+                                const f2 gt = fma2(x.C[k], x.dyh[c], g[c][k]), ht = h[t][c][k];
+                                yc = k == 0 ? mul2(x.C[k], ht) : fma2(x.C[k], ht, yc);
+                                gB = k == 0 ? mul2(x.B[k], gt) : fma2(x.B[k], gt, gB);
+                                dB[k] = c == 0 ? mul2(gt, x.d[c][1]) : fma2(gt, x.d[c][1], dB[k]);
+                                dC[k] = c == 0 ? mul2(ht, x.dyh[c]) : fma2(ht, x.dyh[c], dC[k]);
                                 g[c][k] = mul2(dec[t][c][k], gt);
                                 const f2 w = mul2(g[c][k], t == 0 ? h0[c][k] : h[t - 1][c][k]);
-                                dA[c][k] = fma2(w, d[0], dA[c][k]);
+                                dA[c][k] = fma2(w, x.d[c][0], dA[c][k]);
                                 dd = k == 0 ? mul2(A[c][k], w) : fma2(A[c][k], w, dd);  // A log2(e) here
                             }
-                            const float vy = fold_states<Gm>(sum2(yc)), vg = fold_states<Gm>(sum2(gB)),
-                                        vd = fold_states<Gm>(sum2(dd));
+                            vy[c] = fold_states<Gm>(sum2(yc));
+                            vg[c] = fold_states<Gm>(sum2(gB));
+                            vd[c] = fold_states<Gm>(sum2(dd));
+                        }
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            const int at = (t * CB + c * CL + at0) * NQ + nl;
                             if (nl < NQ) {
-                                o[at * NQ + nl] = vy;
-                                o[Sh::kSum + at * NQ + nl] = vg;
-                                o[2 * Sh::kSum + at * NQ + nl] = vd;
+                                o[at] = vy[c];
+                                o[Sh::kSum + at] = vg[c];
+                                o[2 * Sh::kSum + at] = vd[c];
                             }
                         }
                         sts_quad(o + Sh::bc + ((2 * t) * kWalkers + warp) * 128 + lane * 4, dB);
                         sts_quad(o + Sh::bc + ((2 * t + 1) * kWalkers + warp) * 128 + lane * 4, dC);
+                        x = next;
                     }
                 }
                 __syncthreads();
