@@ -19,7 +19,7 @@ namespace gdr {
 enum { kScanOut = 0, kScanEnds = 1, kScanCkpt = 2 };  // y; chunk maps; states every Seg tokens
 
 template <typename T, typename Gm, int MODE>
-__global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * kFwdBlocks) scan_fwd_kernel(ScanArgs a) {
     constexpr int CH = Gm::CH, LT = Gm::LT, CB = Gm::CB, CL = Gm::CL, NP = Gm::NP;
     constexpr int kIn = 4 * LT * CB + 2 * LT * NP, kOut = LT * CB * Gm::NQ;  // floats of a step: (dt, dt u), B, C; sums
     extern __shared__ __align__(16) float sm[];
@@ -30,10 +30,10 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a) {
     float* const out = sm + 2 * kIn;
 
     if (warp < kWalkers) {
-        const int nl = lane % Gm::NS, cl = lane / Gm::NS, ch0 = warp * Gm::CPW + cl * CH;
+        const int nl = lane % Gm::NS, cl = lane / Gm::NS, p0 = lane_place<Gm>(warp, 0, cl);
         f2 A[CH][2], h[CH][2];
-        load_states<Gm>(A, a.A, tl, a.N, a.state_vec, ch0, nl, kLog2e, true);
-        load_given<Gm>(h, MODE == kScanEnds ? nullptr : a.h0, a, tl, ch0, nl);
+        load_states<Gm>(A, a.A, tl, a.N, a.state_vec, p0, nl, kLog2e, true);
+        load_given<Gm>(h, MODE == kScanEnds ? nullptr : a.h0, a, tl, p0, nl);
         if (MODE != kScanEnds) fold_chunks<Gm>(h, a.ends, a, tl, warp, lane, 0, tl.part, 1);
         f2 total[CH];  // sum of dt
         if (MODE == kScanEnds)
@@ -42,9 +42,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a) {
         __syncthreads();
         for (int s = 0; s <= steps; ++s) {
             if (s < steps) {
-                const float* in = sm + (s & 1) * kIn + lane_place<Gm>(warp, 0, cl) * 4;
+                const float* in = sm + (s & 1) * kIn + p0 * 4;
                 const float* B0 = sm + (s & 1) * kIn + 4 * LT * CB + 4 * nl;
-                float* o = out + (s & 1) * kOut + lane_place<Gm>(warp, 0, cl) * Gm::NQ + nl;
+                float* o = out + (s & 1) * kOut + p0 * Gm::NQ + nl;
                 // a token's operands are loaded before the last one's sums are stored:
                 // the compiler cannot tell that the two do not overlap
                 struct { f2 B[2], C[2], d[CH][2]; } x, next;  // d: dt, dt u
@@ -94,19 +94,21 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a) {
             store_map<Gm>(a.ends, p, h, a, tl, warp, lane);
         }
         const int last = max(seq_len(a.lengths, tl.b, a.T) - 1, 0) / a.chunk;
-        if (MODE == kScanOut && a.h_T && tl.part == last) store_states<Gm>(a.h_T, h, a, tl, ch0, nl);
+        if (MODE == kScanOut && a.h_T && tl.part == last) store_states<Gm>(a.h_T, h, a, tl, p0, nl);
     } else {
-        const int ht = threadIdx.x - 32 * kWalkers, vch = ht % Gm::VPT * 4;
+        const int ht = threadIdx.x - 32 * kWalkers;
         const T* u = reinterpret_cast<const T*>(a.u) + tl.b * a.us[0] + tl.c0;
         const T* dl = reinterpret_cast<const T*>(a.delta) + tl.b * a.ds[0] + tl.c0;
         const T* z = MODE == kScanOut && a.z ? reinterpret_cast<const T*>(a.z) + tl.b * a.zs[0] + tl.c0 : nullptr;
         const T* Bm = reinterpret_cast<const T*>(a.Bm) + tl.b * a.bs[0] + tl.g * a.N;
         const T* Cm = MODE == kScanOut ? reinterpret_cast<const T*>(a.Cm) + tl.b * a.cs[0] + tl.g * a.N : nullptr;
-        T* y = reinterpret_cast<T*>(a.y) + (size_t)tl.b * a.T * a.D_ + tl.c0 + vch;
         using Rows = TokenRows<T, Gm, LT>;
+        constexpr int VW = Rows::VW;
+        const int vch = Rows::channel(ht);
+        T* y = reinterpret_cast<T*>(a.y) + (size_t)tl.b * a.T * a.D_ + tl.c0 + vch;
         Rows ru, rd, rz, held_u[2], held_z[2];  // held: of the steps being walked and put out
         StateRows<T, Gm, LT> rb;
-        float bias[4], skip[4];
+        float bias[VW], skip[VW];
         channel_values(bias, a.bias, tl, vch);
         channel_values(skip, a.D, tl, vch);
         auto fetch = [&](int s) {
@@ -124,15 +126,15 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a) {
             for (int i = 0; i < Rows::NV; ++i) {
                 const int tok = Rows::token(i, ht);
                 const bool on = tl.t0 + s * LT + tok < tl.n && vch < tl.kleft;
-                float raw[4], uf[4], dt[4];
+                float raw[VW], uf[VW], dt[VW];
                 raw_floats(raw, rd.v[i]);
                 raw_floats(uf, ru.v[i]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) raw[j] += bias[j];
+                for (int j = 0; j < VW; ++j) raw[j] += bias[j];
                 step_sizes(dt, raw, a.softplus);
                 if (tok < LT)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < VW; ++j) {
                         const float d = on ? dt[j] : 0.f;
                         const f2 q[2] = {both2(d), both2(d * uf[j])};
                         sts_quad(in + (tok * CB + channel_place<Gm>(vch + j)) * 4, q);
@@ -148,35 +150,38 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a) {
         __syncthreads();
         for (int s = 0; s <= steps; ++s) {
             stage(s + 1);
+            const Rows last_u = held_u[0], last_z = held_z[0];
+            held_u[0] = held_u[1];
+            held_z[0] = held_z[1];
+            held_u[1] = ru;
+            held_z[1] = rz;
+            fetch(s + 2);
             if (MODE == kScanOut && s > 0) {
                 const float* o = out + ((s - 1) & 1) * kOut;
 #pragma unroll
                 for (int i = 0; i < Rows::NV; ++i) {
                     const int tok = Rows::token(i, ht), t = tl.t0 + (s - 1) * LT + tok;
                     if (tok >= LT || t >= tl.t1 || vch >= tl.kleft) continue;
-                    float f[4], uf[4], zf[4];
-                    raw_floats(uf, held_u[0].v[i]);
+                    float f[VW], uf[VW], zf[VW];
+                    raw_floats(uf, last_u.v[i]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < VW; ++j)
                         f[j] = fmaf(skip[j], uf[j],
                                     sum_states<Gm>(o + (tok * CB + channel_place<Gm>(vch + j)) * Gm::NQ));
                     if (z) {
-                        raw_floats(zf, held_z[0].v[i]);
+                        raw_floats(zf, last_z.v[i]);
 #pragma unroll
-                        for (int j = 0; j < 4; j += 2) {
+                        for (int j = 0; j < VW; j += 2) {
                             const f2 zz = pack2(zf[j], zf[j + 1]);
                             unpack2(mul2(mul2(zz, sigmoid2(zz)), pack2(f[j], f[j + 1])), f[j], f[j + 1]);
                         }
                     }
-                    if (t >= tl.n) f[0] = f[1] = f[2] = f[3] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < VW; ++j)
+                        if (t >= tl.n) f[j] = 0.f;
                     store_row(y + (size_t)t * a.D_, f, tl.kleft - vch, a.act_vec);
                 }
             }
-            held_u[0] = held_u[1];
-            held_z[0] = held_z[1];
-            held_u[1] = ru;
-            held_z[1] = rz;
-            fetch(s + 2);
             __syncthreads();
         }
     }
@@ -190,7 +195,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_fwd_kernel(ScanArgs a) {
 }
 
 template <typename T, int NS, int MODE> static cudaError_t launch_fwd_geom(const ScanArgs& a, int B, cudaStream_t st) {
-    using Gm = ScanGeom<NS>;
+    using Gm = std::conditional_t<MODE == kScanCkpt, ScanBwdGeom<NS>, ScanFwdGeom<NS>>;
     const long long grid = (long long)B * a.G * a.tiles * a.chunks;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
     const size_t smem = 2 * (4 * Gm::LT * Gm::CB + 2 * Gm::LT * Gm::NP + Gm::LT * Gm::CB * Gm::NQ) * sizeof(float);
@@ -215,20 +220,20 @@ template <typename F> static cudaError_t dispatch_scan_lanes(int ns, F&& f) {
 // Chunks of the tokens: as many as fill two blocks per SM, of 256 tokens at
 // least, and none below three (see above).
 int scan_chunks(int B, int T, int K, int N, int G) {
-    const long long units = (long long)B * G * scan_tiles(K, N);
-    const long long c = units > 0 ? 296 / units : 0, most = T / 256;
+    const long long units = (long long)B * G * scan_tiles(K, N, 2);
+    const long long c = units > 0 ? 148 * kFwdBlocks / units : 0, most = T / 256;
     const long long n = c < most ? c : most;
     return n < 3 ? 1 : (int)n;
 }
 // Sets the split; a chunk is a whole number of steps and segments.
-void scan_split(ScanArgs& a, int chunks) {
+void scan_split(ScanArgs& a, int chunks, int CH) {
     const int per = (a.T + chunks - 1) / chunks;
     a.chunk = per < 16 ? 16 : (per + 15) / 16 * 16;
     a.chunks = a.T > 0 ? (a.T + a.chunk - 1) / a.chunk : 1;
-    a.tiles = scan_tiles(a.K, a.N);
+    a.tiles = scan_tiles(a.K, a.N, CH);
 }
-size_t scan_ends_bytes(int B, int G, int K, int N, int chunks) {
-    return chunks < 2 ? 0 : (size_t)B * G * scan_tiles(K, N) * chunks * kWalkers * 2 * 256 * sizeof(float);
+size_t scan_ends_bytes(int B, int G, int K, int N, int chunks, int CH) {
+    return chunks < 2 ? 0 : (size_t)B * G * scan_tiles(K, N, CH) * chunks * kWalkers * 2 * CH * 128 * sizeof(float);
 }
 
 template <int MODE> static cudaError_t launch_fwd_mode(const ScanArgs& a, int B, int dtype, cudaStream_t st) {

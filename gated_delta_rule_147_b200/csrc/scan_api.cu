@@ -11,8 +11,8 @@ struct ScanBwdLayout { size_t ckpt, bc, prm, ends, grad_ends, total; };
 ScanBwdLayout scan_bwd_layout(int B, int T, int D, int N, int G, int chunks);
 int scan_chunks(int B, int T, int K, int N, int G);
 int scan_bwd_chunks(int B, int T, int K, int N, int G);
-void scan_split(ScanArgs& a, int chunks);
-size_t scan_ends_bytes(int B, int G, int K, int N, int chunks);
+void scan_split(ScanArgs& a, int chunks, int CH);
+size_t scan_ends_bytes(int B, int G, int K, int N, int chunks, int CH);
 }  // namespace gdr
 
 using namespace gdr;
@@ -67,7 +67,7 @@ extern "C" {
 
 size_t gdr_scan_fwd_workspace_size(int B, int T, int D_, int N, int G) {
     if (B < 1 || T < 0 || D_ < 1 || N < 1 || N > 128 || G < 1 || D_ % G) return 0;
-    return scan_ends_bytes(B, G, D_ / G, N, scan_chunks(B, T, D_ / G, N, G));
+    return scan_ends_bytes(B, G, D_ / G, N, scan_chunks(B, T, D_ / G, N, G), 2);
 }
 
 gdr_status gdr_scan_fwd(const void* u, const void* delta, const float* A, const void* Bm, const void* Cm,
@@ -87,7 +87,7 @@ gdr_status gdr_scan_fwd(const void* u, const void* delta, const float* A, const 
     const size_t need = gdr_scan_fwd_workspace_size(B, T, D_, N, G);
     const bool split = workspace && need && workspace_bytes >= need;
     a.ends = reinterpret_cast<float*>(workspace);
-    scan_split(a, split ? scan_chunks(B, T, a.K, N, G) : 1);
+    scan_split(a, split ? scan_chunks(B, T, a.K, N, G) : 1, 2);
     return launched(launch_scan_fwd(a, B, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 

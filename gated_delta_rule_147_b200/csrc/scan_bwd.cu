@@ -37,7 +37,7 @@ template <typename Gm> struct ScanBwdShared {
 
 // ENDS: the chunk's maps only, its segments in order.
 template <typename T, typename TG, typename Gm, bool ENDS>
-__global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(ScanArgs a) {
     constexpr int CH = Gm::CH, L = Gm::Seg, CB = Gm::CB, CL = Gm::CL, NP = Gm::NP, NS = Gm::NS, NQ = Gm::NQ;
     using Sh = ScanBwdShared<Gm>;
     extern __shared__ __align__(16) float sm[];
@@ -49,9 +49,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
     float* const prm = a.prm + ((size_t)tl.b * a.chunks + tl.part) * a.D_ * (a.N + 2);
 
     if (warp < kWalkers) {
-        const int nl = lane % NS, cl = lane / NS, ch0 = warp * Gm::CPW + cl * CH, at0 = lane_place<Gm>(warp, 0, cl);
+        const int nl = lane % NS, cl = lane / NS, at0 = lane_place<Gm>(warp, 0, cl);
         f2 A[CH][2];
-        load_states<Gm>(A, a.A, tl, a.N, a.state_vec, ch0, nl, kLog2e, true);
+        load_states<Gm>(A, a.A, tl, a.N, a.state_vec, at0, nl, kLog2e, true);
         if constexpr (ENDS) {
             f2 h[CH][2], p[CH][2], E[CH][2];
 #pragma unroll
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
             store_map<Gm>(a.grad_ends, p, E, a, tl, warp, lane);
         } else {
             f2 dA[CH][2], g[CH][2], next[CH][2];
-            load_given<Gm>(g, a.dh_T, a, tl, ch0, nl);
+            load_given<Gm>(g, a.dh_T, a, tl, at0, nl);
             fold_chunks<Gm>(g, a.grad_ends, a, tl, warp, lane, a.chunks - 1, tl.part, -1);
 #pragma unroll
             for (int c = 0; c < CH; ++c) dA[c][0] = dA[c][1] = both2(0.f);
@@ -184,20 +184,24 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
                 }
                 __syncthreads();
             }
-            if (a.dh0 && tl.part == 0) store_states<Gm>(a.dh0, g, a, tl, ch0, nl);
+            if (a.dh0 && tl.part == 0) store_states<Gm>(a.dh0, g, a, tl, at0, nl);
             // dA: this block's part, a lane's own states
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 float f[4];
                 unpack2(dA[c][0], f[0], f[1]);
                 unpack2(dA[c][1], f[2], f[3]);
+                const int ch = place_channel<Gm>(at0 + c * CL);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (ch0 + c < tl.kleft && nl * 4 + i < a.N) prm[(size_t)(tl.c0 + ch0 + c) * a.N + nl * 4 + i] = f[i];
+                    if (ch < tl.kleft && nl * 4 + i < a.N) prm[(size_t)(tl.c0 + ch) * a.N + nl * 4 + i] = f[i];
             }
         }
     } else {
-        const int ht = threadIdx.x - 32 * kWalkers, vch = ht % Gm::VPT * 4;
+        const int ht = threadIdx.x - 32 * kWalkers;
+        using Rows = TokenRows<T, Gm, L>;
+        constexpr int VW = Rows::VW;
+        const int vch = Rows::channel(ht);
         const T* u = reinterpret_cast<const T*>(a.u) + tl.b * a.us[0] + tl.c0;
         const T* dl = reinterpret_cast<const T*>(a.delta) + tl.b * a.ds[0] + tl.c0;
         const T* z = a.z ? reinterpret_cast<const T*>(a.z) + tl.b * a.zs[0] + tl.c0 : nullptr;
@@ -206,12 +210,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
         const T* Cm = reinterpret_cast<const T*>(a.Cm) + tl.b * a.cs[0] + tl.g * a.N;
         const size_t rbase = (size_t)tl.b * a.T * a.D_ + tl.c0 + vch;
         float* bcp = a.bcpart + (((size_t)tl.tile * (gridDim.x / (a.tiles * a.chunks * a.G)) + tl.b) * a.T * a.G + tl.g) * (2 * NP);
-        using Rows = TokenRows<T, Gm, L>;
         Rows ru, rd, rz, held_u[2];  // held: of the segments being walked and put out
         TokenRows<TG, Gm, L> rg;
         StateRows<T, Gm, L> rb;
-        float sig[Rows::NV][4], gz[Rows::NV][4], held_sig[Rows::NV][4], held_gz[Rows::NV][4];  // ddt/ddelta, dy dgate/dz
-        float bias[4], skip[4], dD[4] = {0.f, 0.f, 0.f, 0.f}, db[4] = {0.f, 0.f, 0.f, 0.f};
+        float sig[Rows::NV][VW], gz[Rows::NV][VW], held_sig[Rows::NV][VW], held_gz[Rows::NV][VW];  // ddt/ddelta, dy dgate/dz
+        float bias[VW], skip[VW], dD[VW], db[VW];
+#pragma unroll
+        for (int j = 0; j < VW; ++j) dD[j] = db[j] = 0.f;
         channel_values(bias, a.bias, tl, vch);
         channel_values(skip, a.D, tl, vch);
         auto fetch = [&](int s) {
@@ -230,15 +235,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
             for (int i = 0; i < Rows::NV; ++i) {
                 const int tok = Rows::token(i, ht);
                 const bool on = tl.t0 + segment(s) * L + tok < tl.n && vch < tl.kleft;
-                float raw[4], uf[4], dt[4], g[4];
+                float raw[VW], uf[VW], dt[VW], g[VW];
                 raw_floats(raw, rd.v[i]);
                 raw_floats(uf, ru.v[i]);
                 raw_floats(g, rg.v[i]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) raw[j] += bias[j];
+                for (int j = 0; j < VW; ++j) raw[j] += bias[j];
                 step_sizes(dt, raw, a.softplus);
 #pragma unroll
-                for (int j = 0; j < 4; j += 2) {
+                for (int j = 0; j < VW; j += 2) {
                     if (!ENDS) {
                         f2 sg = both2(1.f);
                         if (a.softplus) sg = sigmoid2(pack2(raw[j], raw[j + 1]));
@@ -256,7 +261,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
                 }
                 if (tok < L)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < VW; ++j) {
                         const float d = on ? dt[j] : 0.f;
                         const f2 q[2] = {both2(d), both2(d * uf[j])};
                         const int at = tok * CB + channel_place<Gm>(vch + j);
@@ -274,10 +279,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
             for (int i = 0; i < Rows::NV; ++i) {
                 const int tok = Rows::token(i, ht), t = t0 + tok;
                 if (tok >= L || t >= tl.t1 || vch >= tl.kleft) continue;
-                float uf[4], du[4], dd[4], dz[4];
+                float uf[VW], du[VW], dd[VW], dz[VW];
                 raw_floats(uf, held_u[0].v[i]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < VW; ++j) {
                     const int at = tok * CB + channel_place<Gm>(vch + j);
                     const float dt = in[at * 4], dyh = in[Sh::dy + at * 2];
                     const float gB = sum_states<Gm>(o + Sh::kSum + at * NQ);
@@ -297,16 +302,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
             // dB, dC over the block's channels: quad e is token e / (2 NS), B or C, 4
             // states; F threads add up to 4 CL terms, each row from another lane on
             // (for the banks)
+            // (threads of a quad start a lane apart too, where each has whole rows)
             constexpr int Q = L * 2 * NS, F = Q < kHelperThreads ? kHelperThreads / Q : 1, kTerms = kWalkers * CL / F;
 #pragma unroll
             for (int q0 = 0; q0 < Q; q0 += kHelperThreads / F) {
                 const int e = q0 + ht / F, row = e / NS, first = ht % F * kTerms, t = t0 + row / 2;
+                const int turn = row + (kTerms % CL ? 0 : ht % F);
                 f2 v[2] = {both2(0.f), both2(0.f)};
 #pragma unroll
                 for (int k = 0; k < kTerms; ++k) {
                     const int term = first + k;
                     f2 x[2];
-                    lds_quad(x, o + Sh::bc + (row * kWalkers + term / CL) * 128 + ((term + row) % CL * NS + e % NS) * 4);
+                    lds_quad(x, o + Sh::bc + (row * kWalkers + term / CL) * 128 + ((term + turn) % CL * NS + e % NS) * 4);
                     v[0] = add2(v[0], x[0]);
                     v[1] = add2(v[1], x[1]);
                 }
@@ -322,12 +329,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
             held_u[0] = held_u[1];
             held_u[1] = ru;
         };
-        float sig1[Rows::NV][4], gz1[Rows::NV][4];  // of the segment being walked
+        float sig1[Rows::NV][VW], gz1[Rows::NV][VW];  // of the segment being walked
         auto hold_factors = [&]() {
 #pragma unroll
             for (int i = 0; i < Rows::NV; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < VW; ++j) {
                     held_sig[i][j] = sig1[i][j];
                     held_gz[i][j] = gz1[i][j];
                     sig1[i][j] = sig[i][j];
@@ -360,12 +367,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_bwd_kernel(ScanArgs a) {
                 if (z) a.dz[o] = 0.f;
             }
             // dD, ddelta_bias: threads of a channel added in order
-            constexpr int kShare = kHelperThreads / Gm::VPT;
+            constexpr int kShare = kHelperThreads / Rows::VPT;
             float* red = sm;  // [dD, db][share][CB]
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                red[ht / Gm::VPT * CB + vch + j] = dD[j];
-                red[(kShare + ht / Gm::VPT) * CB + vch + j] = db[j];
+            for (int j = 0; j < VW; ++j) {
+                red[ht / Rows::VPT * CB + vch + j] = dD[j];
+                red[(kShare + ht / Rows::VPT) * CB + vch + j] = db[j];
             }
             asm volatile("bar.sync 1, %0;" ::"n"(kHelperThreads) : "memory");
             for (int e = ht; e < 2 * CB; e += kHelperThreads) {
@@ -416,26 +423,26 @@ __global__ void __launch_bounds__(256) scan_reduce_kernel(ScanReduce r) {
 }
 
 cudaError_t launch_scan_ckpt(const ScanArgs& a, int B, int dtype, cudaStream_t st);
-void scan_split(ScanArgs& a, int chunks);
-size_t scan_ends_bytes(int B, int G, int K, int N, int chunks);
+void scan_split(ScanArgs& a, int chunks, int CH);
+size_t scan_ends_bytes(int B, int G, int K, int N, int chunks, int CH);
 
-// Chunks of the backward pass: its blocks run one to an SM; the maps cost a
+// Chunks of the backward pass: the maps cost a
 // third walk beside two, so two chunks pay already.
 int scan_bwd_chunks(int B, int T, int K, int N, int G) {
-    const long long units = (long long)B * G * scan_tiles(K, N);
-    const long long c = units > 0 ? 148 / units : 0, most = T / 256;
+    const long long units = (long long)B * G * scan_tiles(K, N, 1);
+    const long long c = units > 0 ? 148 * kBwdBlocks / units : 0, most = T / 256;
     const long long n = c < most ? c : most;
     return n < 2 ? 1 : (int)n;
 }
 
-static int bwd_segments(int T, int N) { const int l = scan_lanes(N) == 1 ? 4 : 8; return (T + l - 1) / l; }
+static int bwd_segments(int T, int N) { const int l = scan_segment(scan_lanes(N)); return (T + l - 1) / l; }
 
 struct ScanBwdLayout { size_t ckpt, bc, prm, ends, grad_ends, total; };
 ScanBwdLayout scan_bwd_layout(int B, int T, int D, int N, int G, int chunks) {
-    const size_t tiles = scan_tiles(D / G, N), np = 4 * scan_lanes(N), ends = scan_ends_bytes(B, G, D / G, N, chunks);
+    const size_t tiles = scan_tiles(D / G, N, 1), np = 4 * scan_lanes(N), ends = scan_ends_bytes(B, G, D / G, N, chunks, 1);
     ScanBwdLayout l;
     l.ckpt = 0;
-    l.bc = l.ckpt + round256((size_t)B * G * tiles * kWalkers * bwd_segments(T, N) * 256 * sizeof(float));
+    l.bc = l.ckpt + round256((size_t)B * G * tiles * kWalkers * bwd_segments(T, N) * ScanBwdGeom<1>::QUADS * sizeof(float));
     l.prm = l.bc + round256(tiles * B * T * G * 2 * np * sizeof(float));
     l.ends = l.prm + round256((size_t)B * chunks * D * (N + 2) * sizeof(float));
     l.grad_ends = l.ends + ends;
@@ -445,7 +452,7 @@ ScanBwdLayout scan_bwd_layout(int B, int T, int D, int N, int G, int chunks) {
 
 template <typename T, typename TG, int NS, bool ENDS>
 static cudaError_t launch_bwd_geom(const ScanArgs& a, int B, cudaStream_t st) {
-    using Gm = ScanGeom<NS>;
+    using Gm = ScanBwdGeom<NS>;
     constexpr size_t smem = ScanBwdShared<Gm>::total * sizeof(float);
     static_assert(smem <= 227 * 1024, "shared memory of a block");
     auto kern = scan_bwd_kernel<T, TG, Gm, ENDS>;
@@ -483,7 +490,7 @@ cudaError_t launch_scan_bwd(ScanArgs a, void* ws, float* dA, float* dB, float* d
     a.ends = reinterpret_cast<float*>(w + l.ends);
     a.grad_ends = reinterpret_cast<float*>(w + l.grad_ends);
     a.segs = bwd_segments(a.T, a.N);
-    scan_split(a, chunks);
+    scan_split(a, chunks, 1);
     if ((long long)B * a.G * a.tiles * a.chunks > 0x7fffffffll) return cudaErrorInvalidValue;
     cudaError_t e = a.chunks > 1 ? launch_bwd_types<true>(a, B, dtype, grad_dtype, st) : cudaSuccess;
     if (e != cudaSuccess) return e;

@@ -58,22 +58,27 @@ struct ScanArgs {
     float *ends, *grad_ends;
 };
 
-template <int NS_> struct ScanGeom {
-    static constexpr int NS = NS_, CH = 2;
+template <int NS_, int CH_, int VW_> struct ScanGeom {
+    static constexpr int NS = NS_, CH = CH_;
     static constexpr int NP = 4 * NS;               // padded states
     static constexpr int CL = 32 / NS;              // channel lanes
     static constexpr int CPW = CH * CL;             // channels of a walker
     static constexpr int CB = kWalkers * CPW;       // channels of a block
     static constexpr int NQ = NS < 4 ? NS : 4;      // partial sums over the states that go to shared memory
     static constexpr int QUADS = CH * 32 * 4;       // floats of a walker's state
-    static constexpr int LT = NS >= 4 ? 16 : NS == 2 ? 8 : 4;  // tokens of a step: bounded by shared memory
-    static constexpr int Seg = NS == 1 ? 4 : 8;     // tokens of a backward segment
-    static constexpr int VPT = CB / 4;              // vectors of 4 channels of a token
+    static constexpr int LT = NS * 4 >= 8 * CH ? 16 : NS * 4 >= 4 * CH ? 8 : 4;  // tokens of a step: bounded by shared memory
+    static constexpr int Seg = NS <= 2 ? 4 : 8;     // tokens of a backward segment, likewise
+    // the helpers move rows in vectors of VW channels
+    static constexpr int VW = VW_ < CB ? VW_ : CB, VPT = CB / VW;
 };
-
-// Vectors of 4 elements that one of the helper threads holds of L token rows.
-template <typename Gm, int L> constexpr int row_vecs() { return L * Gm::VPT > kHelperThreads ? L * Gm::VPT / kHelperThreads : 1; }
-template <typename Gm, int L> constexpr int state_vecs() { return 2 * L * Gm::NS > kHelperThreads ? 2 * L * Gm::NS / kHelperThreads : 1; }
+// Forward: 2 channels a lane and 2 blocks per SM take 478 us for 4 x 4096 tokens
+// x 4096 channels x 16 states, 1 channel and 4 blocks 579, 1 and 3 618. Backward
+// (its checkpoints too): 1 channel and 2 blocks 1130 us for 2 x 4096 x 4096 x 16
+// (ragged), 2 and 1 1325. Vectors: every helper thread has work with 16 states.
+constexpr int kFwdBlocks = 2, kBwdBlocks = 2;
+template <int NS> using ScanFwdGeom = ScanGeom<NS, 2, 4>;
+template <int NS> using ScanBwdGeom = ScanGeom<NS, 1, 2>;
+constexpr int scan_segment(int ns) { return ns <= 2 ? 4 : 8; }
 
 // Block -> (sequence, group, channel tile, chunk of tokens), tile fastest:
 // blocks that share B and C run together. Tokens [t0, n) are this chunk's,
@@ -98,14 +103,27 @@ struct ScanTile {
     }
 };
 
-// One lane's states of its channels (ch0 of the block's on), [D, N] (A) or
+// Place of a block's channel among the values of one token in shared memory:
+// element j of the helpers' vector k at j VPT + k, so that helpers (one j at a
+// time) and walkers (CL adjacent places) both go through the banks in order. With
+// channels in their own order helpers met 4-way conflicts, and the kernel took
+// 1.5 times as long. Walker w holds the places from w CPW on.
+template <typename Gm> __device__ __forceinline__ int channel_place(int ch) { return ch % Gm::VW * Gm::VPT + ch / Gm::VW; }
+template <typename Gm> __device__ __forceinline__ int place_channel(int place) {
+    return place % Gm::VPT * Gm::VW + place / Gm::VPT;
+}
+template <typename Gm> __device__ __forceinline__ int lane_place(int walker, int c, int cl) {
+    return (walker * Gm::CH + c) * Gm::CL + cl;
+}
+
+// One lane's states of its channels (places p0, p0 + CL, ..), [D, N] (A) or
 // [B, D, N] layout.
 template <typename Gm>
 __device__ __forceinline__ void load_states(f2 (&s)[Gm::CH][2], const float* p, const ScanTile& tl, int N, int vec,
-                                            int ch0, int nl, float scale, bool clamp) {
+                                            int p0, int nl, float scale, bool clamp) {
 #pragma unroll
     for (int c = 0; c < Gm::CH; ++c) {
-        const int ch = ch0 + c;
+        const int ch = place_channel<Gm>(p0 + c * Gm::CL);
         float f[4] = {0.f, 0.f, 0.f, 0.f};
         if (ch < tl.kleft && nl * 4 < N) {
             const float* q = p + (size_t)(tl.c0 + ch) * N + nl * 4;
@@ -129,9 +147,9 @@ __device__ __forceinline__ void load_states(f2 (&s)[Gm::CH][2], const float* p, 
 // The state a sequence starts (or a gradient ends) with: p's, or 0 without p.
 template <typename Gm>
 __device__ __forceinline__ void load_given(f2 (&s)[Gm::CH][2], const float* p, const ScanArgs& a, const ScanTile& tl,
-                                           int ch0, int nl) {
+                                           int p0, int nl) {
     if (p) {
-        load_states<Gm>(s, p + (size_t)tl.b * a.D_ * a.N, tl, a.N, a.state_vec, ch0, nl, 1.f, false);
+        load_states<Gm>(s, p + (size_t)tl.b * a.D_ * a.N, tl, a.N, a.state_vec, p0, nl, 1.f, false);
     } else {
 #pragma unroll
         for (int c = 0; c < Gm::CH; ++c) s[c][0] = s[c][1] = both2(0.f);
@@ -139,10 +157,10 @@ __device__ __forceinline__ void load_given(f2 (&s)[Gm::CH][2], const float* p, c
 }
 template <typename Gm>
 __device__ __forceinline__ void store_states(float* p, const f2 (&s)[Gm::CH][2], const ScanArgs& a, const ScanTile& tl,
-                                             int ch0, int nl) {
+                                             int p0, int nl) {
 #pragma unroll
     for (int c = 0; c < Gm::CH; ++c) {
-        const int ch = ch0 + c;
+        const int ch = place_channel<Gm>(p0 + c * Gm::CL);
         if (ch >= tl.kleft || nl * 4 >= a.N) continue;
         float f[4];
         unpack2(s[c][0], f[0], f[1]);
@@ -157,15 +175,17 @@ __device__ __forceinline__ void store_states(float* p, const f2 (&s)[Gm::CH][2],
 }
 
 // [L tokens][CB channels] of one input among the helpers: vector i of thread
-// `ht` is number v = 128 i + ht, token v / VPT, channels from (v % VPT) 4 (the
+// `ht` is number v = 128 i + ht, token v / VPT, channels from (v % VPT) VW (the
 // same for every i). Tokens from n on and channels beyond the tile are not read
 // and give 0.
 template <typename T, typename Gm, int L> struct TokenRows {
-    static constexpr int NV = row_vecs<Gm, L>();
-    RawVec<T, 4> v[NV];
-    static __device__ __forceinline__ int token(int i, int ht) { return (kHelperThreads * i + ht) / Gm::VPT; }
+    static constexpr int VW = Gm::VW, VPT = Gm::VPT;
+    static constexpr int NV = L * VPT > kHelperThreads ? L * VPT / kHelperThreads : 1;
+    RawVec<T, VW> v[NV];
+    static __device__ __forceinline__ int token(int i, int ht) { return (kHelperThreads * i + ht) / VPT; }
+    static __device__ __forceinline__ int channel(int ht) { return ht % VPT * VW; }
     __device__ __forceinline__ void fetch(const T* p, long long st, int t0, const ScanTile& tl, int vec, int ht) {
-        const int ch = ht % Gm::VPT * 4;
+        const int ch = channel(ht);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int tok = token(i, ht);
@@ -175,27 +195,22 @@ template <typename T, typename Gm, int L> struct TokenRows {
             if (vec) v[i].load(q);
             else
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < VW; ++j)
                     if (ch + j < tl.kleft) v[i].set(j, q[j]);
         }
     }
 };
-template <typename T, bool VEC4>
-__device__ __forceinline__ void store_row(T* p, const float (&f)[4], int left) {
-    if constexpr (VEC4) VecIO<T, 4>::store(p, f);
+template <typename T, int VW> __device__ __forceinline__ void store_row(T* p, const float (&f)[VW], int left, int vec) {
+    if (vec) VecIO<T, VW>::store(p, f);
     else
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < VW; ++j)
             if (j < left) p[j] = from_f32<T>(f[j]);
-}
-template <typename T> __device__ __forceinline__ void store_row(T* p, const float (&f)[4], int left, int vec) {
-    if (vec) store_row<T, true>(p, f, left);
-    else store_row<T, false>(p, f, left);
 }
 
 // [L tokens][N states] of B and of C behind it, staged as fp32 rows of NP.
 template <typename T, typename Gm, int L> struct StateRows {
-    static constexpr int NV = state_vecs<Gm, L>(), kEach = L * Gm::NS;
+    static constexpr int kEach = L * Gm::NS, NV = 2 * kEach > kHelperThreads ? 2 * kEach / kHelperThreads : 1;
     RawVec<T, 4> v[NV];
     __device__ __forceinline__ void fetch(const T* Bp, const T* Cp, const ScanArgs& a, int t0, const ScanTile& tl,
                                           int ht) {
@@ -224,34 +239,24 @@ template <typename T, typename Gm, int L> struct StateRows {
     }
 };
 
-template <typename T> __device__ __forceinline__ void raw_floats(float (&f)[4], const RawVec<T, 4>& r) {
+template <typename T, int VW> __device__ __forceinline__ void raw_floats(float (&f)[VW], const RawVec<T, VW>& r) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = r.get(i);
+    for (int i = 0; i < VW; ++i) f[i] = r.get(i);
 }
-// dt of 4 raw steps.
-__device__ __forceinline__ void step_sizes(float (&dt)[4], const float (&raw)[4], int softplus) {
-    if (softplus) {
-        unpack2(softplus2(pack2(raw[0], raw[1])), dt[0], dt[1]);
-        unpack2(softplus2(pack2(raw[2], raw[3])), dt[2], dt[3]);
-    } else {
+// dt of raw steps.
+template <int VW> __device__ __forceinline__ void step_sizes(float (&dt)[VW], const float (&raw)[VW], int softplus) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dt[i] = raw[i];
+    for (int i = 0; i < VW; i += 2) {
+        dt[i] = raw[i];
+        dt[i + 1] = raw[i + 1];
+        if (softplus) unpack2(softplus2(pack2(raw[i], raw[i + 1])), dt[i], dt[i + 1]);
     }
 }
-// Four channels' values from a [D] array, 0 where absent.
-__device__ __forceinline__ void channel_values(float (&f)[4], const float* p, const ScanTile& tl, int ch) {
+// Channels' values from a [D] array, 0 where absent.
+template <int VW>
+__device__ __forceinline__ void channel_values(float (&f)[VW], const float* p, const ScanTile& tl, int ch) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = p && ch + j < tl.kleft ? p[tl.c0 + ch + j] : 0.f;
-}
-
-// Place of a block's channel among the values of one token, in the order the
-// walkers' lanes read them: walker, channel of the lane, lane.
-template <typename Gm> __device__ __forceinline__ int channel_place(int ch) {
-    const int in = ch % Gm::CPW;
-    return (ch / Gm::CPW * Gm::CH + in % Gm::CH) * Gm::CL + in / Gm::CH;
-}
-template <typename Gm> __device__ __forceinline__ int lane_place(int walker, int c, int cl) {
-    return (walker * Gm::CH + c) * Gm::CL + cl;
+    for (int j = 0; j < VW; ++j) f[j] = p && ch + j < tl.kleft ? p[tl.c0 + ch + j] : 0.f;
 }
 
 // Partial sums over the states: lanes whose numbers differ in bits above the
@@ -307,6 +312,10 @@ inline int scan_lanes(int N) {
     while (4 * ns < N) ns *= 2;
     return ns;
 }
-inline int scan_tiles(int K, int N) { const int cb = kWalkers * 64 / scan_lanes(N); return (K + cb - 1) / cb; }
+// Blocks' tiles of a group's K channels, at CH channels a lane.
+inline int scan_tiles(int K, int N, int CH) {
+    const int cb = kWalkers * CH * 32 / scan_lanes(N);
+    return (K + cb - 1) / cb;
+}
 
 }  // namespace gdr

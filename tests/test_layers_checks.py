@@ -165,10 +165,10 @@ def test_workspace_sizes():
     assert _lib.gdr_conv_bwd_workspace_size(1, 0, 8, 4) == 256
     assert _lib.gdr_conv_bwd_workspace_size(2, 16, 512, 4) == 2 * 5 * 512 * 4
     assert _lib.gdr_conv_bwd_workspace_size(2, 16, 512, 5) == 0
-    # scan: 64 channels x 16 states every 8 tokens; dB and dC of the one tile; parameters
-    assert _lib.gdr_scan_bwd_workspace_size(1, 20, 16, 16, 1) == 3 * 4096 + 20 * 32 * 4 + 1280
+    # scan: 32 channels x 16 states every 8 tokens; dB and dC of the one tile; parameters
+    assert _lib.gdr_scan_bwd_workspace_size(1, 20, 16, 16, 1) == 3 * 2048 + 20 * 32 * 4 + 1280
     # the same split in two chunks, with the maps of each (decay and end, twice)
-    assert _lib.gdr_scan_bwd_workspace_size(1, 512, 16, 16, 1) == 64 * 4096 + 512 * 32 * 4 + 2304 + 2 * 2 * 8192
+    assert _lib.gdr_scan_bwd_workspace_size(1, 512, 16, 16, 1) == 64 * 2048 + 512 * 32 * 4 + 2304 + 2 * 2 * 4096
     assert _lib.gdr_scan_fwd_workspace_size(1, 767, 16, 16, 1) == 0  # two chunks of 256 do not pay
     assert _lib.gdr_scan_fwd_workspace_size(1, 768, 16, 16, 1) == 3 * 8192
     assert _lib.gdr_scan_fwd_workspace_size(4, 4096, 4096, 16, 1) == 0
