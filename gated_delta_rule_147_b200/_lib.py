@@ -213,31 +213,6 @@ def gdr_decode_step(q, k, v, alpha, b, w, alpha_kind, b_kind, w_kind, S, o, B, H
         raise GdrError("gdr_decode_step", st)
 
 
-def _layer_call(name, argc):
-    """A layer entry point: the C arguments in their order, tensors by device
-    pointer, then the stream. `argc` counts them without the stream."""
-    def call(*args, stream=None) -> None:
-        if len(args) != argc:
-            raise TypeError(f"{name} takes {argc} arguments and the stream, got {len(args)}")
-        st = getattr(_handle or load(), name)(*[a.data_ptr() if hasattr(a, "data_ptr") else a for a in args],
-                                              _stream(stream))
-        if st != GDR_OK:
-            raise GdrError(name, st)
-    call.__name__ = call.__qualname__ = name
-    call.__doc__ = f"Same arguments as the C entry point {name} (include/gdr.h)."
-    return call
-
-
-gdr_conv_fwd = _layer_call("gdr_conv_fwd", 15)
-gdr_conv_bwd = _layer_call("gdr_conv_bwd", 22)
-gdr_conv_step = _layer_call("gdr_conv_step", 12)
-gdr_scan_fwd = _layer_call("gdr_scan_fwd", 22)
-gdr_scan_bwd = _layer_call("gdr_scan_bwd", 32)
-gdr_scan_step = _layer_call("gdr_scan_step", 17)
-gdr_qk_norm_fwd = _layer_call("gdr_qk_norm_fwd", 23)
-gdr_qk_norm_bwd = _layer_call("gdr_qk_norm_bwd", 30)
-
-
 def gdr_conv_bwd_workspace_size(B, T, D, W) -> int:
     return int(load().gdr_conv_bwd_workspace_size(B, T, D, W))
 

@@ -1,15 +1,18 @@
-"""Builds the CUDA library in-tree: gated_delta_rule_147_b200/libgdr.so (sm_100a).
+"""Builds the CUDA library in-tree: gated_delta_rule_147_b200/libgdr.so (sm_100a),
+and the Python module of the layer operators beside it, _layers.so.
 
 Each source compiles to its own object (in parallel, under _build/), then one
-link step makes the shared library.
+link step each makes the shared library and the module (which links to it).
 
 Usage: python -m gated_delta_rule_147_b200.build [--force] [--verbose]
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,7 +24,9 @@ SOURCES = ["api.cu", "decode.cu", "recurrent.cu", "chunk_sm100.cu", "chunk_erase
            "chunk_twopass_sm100.cu", "chunk_twopass256_sm100.cu", "chunk_twopass_general_sm100.cu", "selftest.cu",
            "static_scratch.cu", "conv.cu", "scan.cu", "scan_bwd.cu", "scan_api.cu", "qk_norm.cu"]
 HEADERS = ["common.cuh", "chunk_common.cuh", "rcp_seed.h", "layer_common.cuh", "scan_common.cuh"]
+BINDING = "layers_binding.cpp"
 LIB = os.path.join(HERE, "libgdr.so")
+MODULE = os.path.join(HERE, "_layers.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMPILE_FLAGS = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                  "--expt-relaxed-constexpr"]
@@ -35,15 +40,15 @@ def _nvcc() -> str:
 
 
 def _deps():
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [BINDING]]
     deps.append(os.path.join(ROOT, "include", "gdr.h"))
     return deps
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MODULE):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
     return any(os.path.getmtime(d) > t for d in _deps())
 
 
@@ -57,7 +62,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     inc = ["-I", os.path.join(ROOT, "include")]
     # a header change rebuilds every object; otherwise only sources newer than their object
-    hdr_t = max(os.path.getmtime(d) for d in _deps() if not d.endswith(".cu"))
+    hdr_t = max(os.path.getmtime(d) for d in _deps() if not d.endswith((".cu", ".cpp")))
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)  # not imported: only its headers are wanted
+    cxx = os.environ.get("CXX", "g++")
 
     def compile_one(src: str):
         obj = _obj(src)
@@ -65,16 +72,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if not force and os.path.exists(obj) and os.path.getmtime(obj) > max(os.path.getmtime(path), hdr_t):
             return
         cmd = [_nvcc(), *COMPILE_FLAGS, *inc, "-c", "-o", obj, path]
+        if src == BINDING:
+            dirs = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include/torch/csrc/api/include"),
+                    sysconfig.get_paths()["include"], "/usr/local/cuda/include"]
+            cmd = [cxx, "-O2", "-std=c++17", "-fPIC", *inc, *(f for d in dirs for f in ("-isystem", d)), "-c", "-o", obj,
+                   path]
         if verbose:
-            cmd.insert(1, "-Xptxas=-v")
+            if src != BINDING:
+                cmd.insert(1, "-Xptxas=-v")
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
 
-    with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
-        for f in [ex.submit(compile_one, s) for s in SOURCES]:
+    with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        for f in [ex.submit(compile_one, s) for s in [BINDING, *SOURCES]]:
             f.result()
     link = [_nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", LIB, *[_obj(s) for s in SOURCES]]
     subprocess.run(link, check=True)
+    libs = ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+    subprocess.run([cxx, "-shared", "-o", MODULE, _obj(BINDING), LIB, "-L", os.path.join(torch_dir, "lib"), *libs,
+                    "-Wl,-rpath,$ORIGIN"], check=True)
     return LIB
 
 

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import gated_delta_rule_147_b200 as gdr
-from gated_delta_rule_147_b200 import _lib, layers
+from gated_delta_rule_147_b200 import _layers, _lib, layers  # noqa: F401
 
 P, N = 1 << 20, None  # a fake, aligned device address that no check follows
 BAD, UNSUP, MIS = _lib.GDR_ERR_INVALID_ARG, _lib.GDR_ERR_UNSUPPORTED, _lib.GDR_ERR_MISALIGNED
@@ -34,28 +34,31 @@ def test_wrappers_refuse_host_tensors_and_types():
 ])
 def test_tensor_check(bad, match):
     with pytest.raises((TypeError, ValueError), match=match):
-        layers._check("x", bad(), (2, 4, 8), (torch.bfloat16,), torch.device("cpu"))
+        _layers.check_tensor("x", bad(), (2, 4, 8), 1)
 
 
 def test_tensor_check_takes_slices():
     x = t(2, 4, 24)[..., 8:16]
-    assert layers._check("x", x, (2, 4, 8), (torch.bfloat16,), torch.device("cpu")) == (96, 24, 1)
+    assert _layers.check_tensor("x", x, (2, 4, 8), 1) == (96, 24, 1)
     m = t(2, 4, 20)[..., 4:12].view(2, 4, 2, 4)
-    assert layers._check("m", m, (2, 4, 2, 4), (torch.bfloat16,), torch.device("cpu"), 2)[:2] == (80, 20)
+    assert _layers.check_tensor("m", m, (2, 4, 2, 4), 2)[:2] == (80, 20)
     with pytest.raises(ValueError, match="last 2 axes"):
-        layers._check("m", t(2, 4, 2, 8)[..., :4], (2, 4, 2, 4), (torch.bfloat16,), torch.device("cpu"), 2)
+        _layers.check_tensor("m", t(2, 4, 2, 8)[..., :4], (2, 4, 2, 4), 2)
 
 
 def test_results_stand_apart():
     a = t(4, 8)
-    layers._apart("out", a[:2], (("x", a[2:]), ("X0", None), ("y", t(0, 8))))
-    layers._apart("X_T", a, (("X0", a),), a)
+    apart = _layers.check_apart
+    apart("out", a[:2], "x", a[2:], False)
+    apart("out", a[:2], "X0", None, False)
+    apart("out", a[:2], "y", t(0, 8), False)
     with pytest.raises(ValueError, match="out overlaps x"):
-        layers._apart("out", a[:2], (("x", a[1:]),))
+        apart("out", a[:2], "x", a[1:], False)
     with pytest.raises(ValueError, match="overlaps"):  # a slice between the rows' other elements
-        layers._apart("out", a.view(-1)[4:8], (("x", a[:, :4]),))
+        apart("out", a.view(-1)[4:8], "x", a[:, :4], False)
+    apart("X_T", a, "X0", a, True)
     with pytest.raises(ValueError, match="overlaps"):  # the same start, not the same memory
-        layers._apart("X_T", a.view(-1)[:16], (("X0", a[:, :4]),), None)
+        apart("X_T", a.view(-1)[:16], "X0", a[:, :4], True)
 
 
 def conv(fn="fwd", **kw):
