@@ -196,10 +196,18 @@ __device__ __forceinline__ f2 softplus2(f2 x) {
     r = fma2(r, y, both2(0.9999999403953552f));
     return fma2(r, y, pack2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
 }
-__device__ __forceinline__ float softplus1(float x) {
-    float a, b;
-    unpack2(softplus2(pack2(x, x)), a, b);
-    return a;
+__device__ __forceinline__ float softplusf(float x) {
+    const float y = ex2_approx(-fabsf(x) * kLog2e);
+    float r = 0.0052326940931379795f;
+    r = fmaf(r, y, -0.029505237936973572f);
+    r = fmaf(r, y, 0.07822594791650772f);
+    r = fmaf(r, y, -0.13663245737552643f);
+    r = fmaf(r, y, 0.19106006622314453f);
+    r = fmaf(r, y, -0.2484298199415207f);
+    r = fmaf(r, y, 0.3331909775733948f);
+    r = fmaf(r, y, -0.4999949336051941f);
+    r = fmaf(r, y, 0.9999999403953552f);
+    return fmaf(r, y, fmaxf(x, 0.f));
 }
 
 // V channels (even) of one row, as loaded: wide loads (VEC), or one element at

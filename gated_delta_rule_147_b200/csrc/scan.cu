@@ -18,10 +18,21 @@ namespace gdr {
 
 enum { kScanOut = 0, kScanEnds = 1, kScanCkpt = 2 };  // y; chunk maps; states every Seg tokens
 
+// Words of shared memory: two steps of inputs (dt, dt u; B, C) and of sums, and
+// of rows on their way (delta, u, z; B and C).
+template <typename T, typename Gm> struct ScanFwdShared {
+    static constexpr int LT = Gm::LT;
+    static constexpr int in = 4 * LT * Gm::CB + 2 * LT * Gm::NP, out = LT * Gm::CB * Gm::NQ;
+    using Rows = TokenRows<T, Gm, LT>;
+    using States = StateRows<T, Gm, LT>;
+    static constexpr int slots = 3 * Rows::kWords + States::kWords, total = 2 * (in + out + slots);
+};
+
 template <typename T, typename Gm, int MODE>
 __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * kFwdBlocks) scan_fwd_kernel(ScanArgs a) {
     constexpr int CH = Gm::CH, LT = Gm::LT, CB = Gm::CB, CL = Gm::CL, NP = Gm::NP;
-    constexpr int kIn = 4 * LT * CB + 2 * LT * NP, kOut = LT * CB * Gm::NQ;  // floats of a step: (dt, dt u), B, C; sums
+    using Sh = ScanFwdShared<T, Gm>;
+    constexpr int kIn = Sh::in, kOut = Sh::out;
     extern __shared__ __align__(16) float sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const ScanTile tl(a, CB);
@@ -102,60 +113,67 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
         const T* z = MODE == kScanOut && a.z ? reinterpret_cast<const T*>(a.z) + tl.b * a.zs[0] + tl.c0 : nullptr;
         const T* Bm = reinterpret_cast<const T*>(a.Bm) + tl.b * a.bs[0] + tl.g * a.N;
         const T* Cm = MODE == kScanOut ? reinterpret_cast<const T*>(a.Cm) + tl.b * a.cs[0] + tl.g * a.N : nullptr;
-        using Rows = TokenRows<T, Gm, LT>;
+        using Rows = typename Sh::Rows;
         constexpr int VW = Rows::VW;
         const int vch = Rows::channel(ht);
         T* y = reinterpret_cast<T*>(a.y) + (size_t)tl.b * a.T * a.D_ + tl.c0 + vch;
-        Rows ru, rd, rz, held_u[2], held_z[2];  // held: of the steps being walked and put out
-        StateRows<T, Gm, LT> rb;
+        using States = typename Sh::States;
+        Rows held_u[2], held_z[2];  // of the steps staged and walked
+        uint32_t* const slots = reinterpret_cast<uint32_t*>(out + 2 * kOut);
         float bias[VW], skip[VW];
         channel_values(bias, a.bias, tl, vch);
         channel_values(skip, a.D, tl, vch);
-        auto fetch = [&](int s) {
-            if (s >= steps) return;
-            const int t0 = tl.t0 + s * LT;
-            rd.fetch(dl, a.ds[1], t0, tl, a.act_vec, ht);
-            ru.fetch(u, a.us[1], t0, tl, a.act_vec, ht);
-            rb.fetch(Bm, Cm, a, t0, tl, ht);
-            if (z) rz.fetch(z, a.zs[1], t0, tl, a.act_vec, ht);
+        auto fetch = [&](int s) {  // into the slots of step s - 2
+            uint32_t* w = slots + (s & 1) * Sh::slots;
+            if (s < steps) {
+                const int t0 = tl.t0 + s * LT;
+                Rows::fetch(w, dl, a.ds[1], t0, tl, a.act_vec, ht);
+                Rows::fetch(w + Rows::kWords, u, a.us[1], t0, tl, a.act_vec, ht);
+                if (z) Rows::fetch(w + 2 * Rows::kWords, z, a.zs[1], t0, tl, a.act_vec, ht);
+                States::fetch(w + 3 * Rows::kWords, Bm, Cm, a, t0, tl, ht);
+            }
+            copies_commit();
         };
         auto stage = [&](int s) {
-            if (s >= steps) return;
-            float* in = sm + (s & 1) * kIn;
-#pragma unroll
-            for (int i = 0; i < Rows::NV; ++i) {
-                const int tok = Rows::token(i, ht);
-                const bool on = tl.t0 + s * LT + tok < tl.n && vch < tl.kleft;
-                float raw[VW], uf[VW], dt[VW];
-                raw_floats(raw, rd.v[i]);
-                raw_floats(uf, ru.v[i]);
-#pragma unroll
-                for (int j = 0; j < VW; ++j) raw[j] += bias[j];
-                step_sizes(dt, raw, a.softplus);
-                if (tok < LT)
-#pragma unroll
-                    for (int j = 0; j < VW; ++j) {
-                        const float d = on ? dt[j] : 0.f;
-                        const f2 q[2] = {both2(d), both2(d * uf[j])};
-                        sts_quad(in + (tok * CB + channel_place<Gm>(vch + j)) * 4, q);
-                    }
-            }
-            rb.stage(in + 4 * LT * CB, ht);
-        };
-        fetch(0);
-        stage(0);
-        held_u[1] = ru;
-        held_z[1] = rz;
-        fetch(1);
-        __syncthreads();
-        for (int s = 0; s <= steps; ++s) {
-            stage(s + 1);
-            const Rows last_u = held_u[0], last_z = held_z[0];
             held_u[0] = held_u[1];
             held_z[0] = held_z[1];
-            held_u[1] = ru;
-            held_z[1] = rz;
+            copies_wait<1>();
+            if (s < steps) {
+                float* in = sm + (s & 1) * kIn;
+                const uint32_t* w = slots + (s & 1) * Sh::slots;
+                Rows rd;
+                rd.read(w, ht);
+                held_u[1].read(w + Rows::kWords, ht);
+                if (z) held_z[1].read(w + 2 * Rows::kWords, ht);
+#pragma unroll
+                for (int i = 0; i < Rows::NV; ++i) {
+                    const int tok = Rows::token(i, ht);
+                    const bool on = tl.t0 + s * LT + tok < tl.n && vch < tl.kleft;
+                    float raw[VW], uf[VW], dt[VW];
+                    raw_floats(raw, rd.v[i]);
+                    raw_floats(uf, held_u[1].v[i]);
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) raw[j] += bias[j];
+                    step_sizes(dt, raw, a.softplus);
+                    if (tok < LT)
+#pragma unroll
+                        for (int j = 0; j < VW; ++j) {
+                            const float d = on ? dt[j] : 0.f;
+                            const f2 q[2] = {both2(d), both2(d * uf[j])};
+                            sts_quad(in + (tok * CB + channel_place<Gm>(vch + j)) * 4, q);
+                        }
+                }
+                States::stage(w + 3 * Rows::kWords, in + 4 * LT * CB, ht, MODE == kScanOut);
+            }
             fetch(s + 2);
+        };
+        fetch(0);
+        fetch(1);
+        stage(0);
+        __syncthreads();
+        for (int s = 0; s <= steps; ++s) {
+            const Rows last_u = held_u[0], last_z = held_z[0];
+            stage(s + 1);
             if (MODE == kScanOut && s > 0) {
                 const float* o = out + ((s - 1) & 1) * kOut;
 #pragma unroll
@@ -198,7 +216,8 @@ template <typename T, int NS, int MODE> static cudaError_t launch_fwd_geom(const
     using Gm = std::conditional_t<MODE == kScanCkpt, ScanBwdGeom<NS>, ScanFwdGeom<NS>>;
     const long long grid = (long long)B * a.G * a.tiles * a.chunks;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-    const size_t smem = 2 * (4 * Gm::LT * Gm::CB + 2 * Gm::LT * Gm::NP + Gm::LT * Gm::CB * Gm::NQ) * sizeof(float);
+    constexpr size_t smem = ScanFwdShared<T, Gm>::total * sizeof(float);
+    static_assert(smem <= 227 * 1024, "shared memory of a block");
     auto kern = scan_fwd_kernel<T, Gm, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -323,7 +342,7 @@ __global__ void __launch_bounds__(256, kStepBlocks) scan_step_kernel(ScanArgs a,
                     if (n0 + i < a.N) { s[k][i] = hp[ch * a.N + i]; A[k][i] = Ap[ch * a.N + i]; }
             }
         }
-        if (s0 == 0) dt = !own ? 0.f : a.softplus ? softplus1(raw) : raw;
+        if (s0 == 0) dt = !own ? 0.f : a.softplus ? softplusf(raw) : raw;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int ch = (s0 + k) * CL + cl;

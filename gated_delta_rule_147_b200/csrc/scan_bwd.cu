@@ -26,20 +26,25 @@ namespace gdr {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <typename Gm> struct ScanBwdShared {
+template <typename T, typename TG, typename Gm> struct ScanBwdShared {
     static constexpr int L = Gm::Seg;
     // floats of a step: (dt, dt u) quads, dyh pairs, B, C
     static constexpr int dy = 4 * L * Gm::CB, B = dy + 2 * L * Gm::CB, in = B + 2 * L * Gm::NP;
     // of its results: sums of C h, g B and A a g h over the states, terms of dB and dC
     static constexpr int kSum = L * Gm::CB * Gm::NQ, bc = 3 * kSum, out = bc + L * 2 * kWalkers * 128;
-    static constexpr int total = 2 * (in + out);
+    // of rows on their way: delta, u, z; dy; B and C
+    using Rows = TokenRows<T, Gm, L>;
+    using Grads = TokenRows<TG, Gm, L>;
+    using States = StateRows<T, Gm, L>;
+    static constexpr int slots = 3 * Rows::kWords + Grads::kWords + States::kWords;
+    static constexpr int total = 2 * (in + out + slots);
 };
 
 // ENDS: the chunk's maps only, its segments in order.
 template <typename T, typename TG, typename Gm, bool ENDS>
 __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(ScanArgs a) {
     constexpr int CH = Gm::CH, L = Gm::Seg, CB = Gm::CB, CL = Gm::CL, NP = Gm::NP, NS = Gm::NS, NQ = Gm::NQ;
-    using Sh = ScanBwdShared<Gm>;
+    using Sh = ScanBwdShared<T, TG, Gm>;
     extern __shared__ __align__(16) float sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const ScanTile tl(a, CB);
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
         }
     } else {
         const int ht = threadIdx.x - 32 * kWalkers;
-        using Rows = TokenRows<T, Gm, L>;
+        using Rows = typename Sh::Rows;
         constexpr int VW = Rows::VW;
         const int vch = Rows::channel(ht);
         const T* u = reinterpret_cast<const T*>(a.u) + tl.b * a.us[0] + tl.c0;
@@ -210,66 +215,83 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
         const T* Cm = reinterpret_cast<const T*>(a.Cm) + tl.b * a.cs[0] + tl.g * a.N;
         const size_t rbase = (size_t)tl.b * a.T * a.D_ + tl.c0 + vch;
         float* bcp = a.bcpart + (((size_t)tl.tile * (gridDim.x / (a.tiles * a.chunks * a.G)) + tl.b) * a.T * a.G + tl.g) * (2 * NP);
-        Rows ru, rd, rz, held_u[2];  // held: of the segments being walked and put out
-        TokenRows<TG, Gm, L> rg;
-        StateRows<T, Gm, L> rb;
-        float sig[Rows::NV][VW], gz[Rows::NV][VW], held_sig[Rows::NV][VW], held_gz[Rows::NV][VW];  // ddt/ddelta, dy dgate/dz
+        using Grads = typename Sh::Grads;
+        using States = typename Sh::States;
+        // what the output needs of the segments staged and walked: u, ddt/ddelta,
+        // dy dgate/dz
+        struct Held { Rows u; float sig[Rows::NV][VW], gz[Rows::NV][VW]; } held[2];
+        uint32_t* const slots = reinterpret_cast<uint32_t*>(results + 2 * Sh::out);
         float bias[VW], skip[VW], dD[VW], db[VW];
 #pragma unroll
         for (int j = 0; j < VW; ++j) dD[j] = db[j] = 0.f;
         channel_values(bias, a.bias, tl, vch);
         channel_values(skip, a.D, tl, vch);
-        auto fetch = [&](int s) {
-            if (s >= steps) return;
-            const int t0 = tl.t0 + segment(s) * L;
-            rd.fetch(dl, a.ds[1], t0, tl, a.act_vec, ht);
-            ru.fetch(u, a.us[1], t0, tl, a.act_vec, ht);
-            rb.fetch(Bm, Cm, a, t0, tl, ht);
-            rg.fetch(dy, a.gs[1], t0, tl, a.act_vec, ht);
-            if (z) rz.fetch(z, a.zs[1], t0, tl, a.act_vec, ht);
+        constexpr int kGrads = 3 * Rows::kWords, kStates = kGrads + Grads::kWords;
+        auto fetch = [&](int s) {  // into the slots of step s - 2
+            uint32_t* w = slots + (s & 1) * Sh::slots;
+            if (s < steps) {
+                const int t0 = tl.t0 + segment(s) * L;
+                Rows::fetch(w, dl, a.ds[1], t0, tl, a.act_vec, ht);
+                Rows::fetch(w + Rows::kWords, u, a.us[1], t0, tl, a.act_vec, ht);
+                if (z) Rows::fetch(w + 2 * Rows::kWords, z, a.zs[1], t0, tl, a.act_vec, ht);
+                Grads::fetch(w + kGrads, dy, a.gs[1], t0, tl, a.act_vec, ht);
+                States::fetch(w + kStates, Bm, Cm, a, t0, tl, ht);
+            }
+            copies_commit();
         };
         auto stage = [&](int s) {
-            if (s >= steps) return;
-            float* in = sm + (s & 1) * Sh::in;
+            held[0] = held[1];
+            copies_wait<1>();
+            if (s < steps) {
+                float* in = sm + (s & 1) * Sh::in;
+                const uint32_t* w = slots + (s & 1) * Sh::slots;
+                Rows rd, rz;
+                Grads rg;
+                rd.read(w, ht);
+                held[1].u.read(w + Rows::kWords, ht);
+                if (z) rz.read(w + 2 * Rows::kWords, ht);
+                rg.read(w + kGrads, ht);
 #pragma unroll
-            for (int i = 0; i < Rows::NV; ++i) {
-                const int tok = Rows::token(i, ht);
-                const bool on = tl.t0 + segment(s) * L + tok < tl.n && vch < tl.kleft;
-                float raw[VW], uf[VW], dt[VW], g[VW];
-                raw_floats(raw, rd.v[i]);
-                raw_floats(uf, ru.v[i]);
-                raw_floats(g, rg.v[i]);
+                for (int i = 0; i < Rows::NV; ++i) {
+                    const int tok = Rows::token(i, ht);
+                    const bool on = tl.t0 + segment(s) * L + tok < tl.n && vch < tl.kleft;
+                    float raw[VW], uf[VW], dt[VW], g[VW];
+                    raw_floats(raw, rd.v[i]);
+                    raw_floats(uf, held[1].u.v[i]);
+                    raw_floats(g, rg.v[i]);
 #pragma unroll
-                for (int j = 0; j < VW; ++j) raw[j] += bias[j];
-                step_sizes(dt, raw, a.softplus);
+                    for (int j = 0; j < VW; ++j) raw[j] += bias[j];
+                    step_sizes(dt, raw, a.softplus);
 #pragma unroll
-                for (int j = 0; j < VW; j += 2) {
-                    if (!ENDS) {
-                        f2 sg = both2(1.f);
-                        if (a.softplus) sg = sigmoid2(pack2(raw[j], raw[j + 1]));
-                        unpack2(sg, sig[i][j], sig[i][j + 1]);
+                    for (int j = 0; j < VW; j += 2) {
+                        if (!ENDS) {
+                            f2 sg = both2(1.f);
+                            if (a.softplus) sg = sigmoid2(pack2(raw[j], raw[j + 1]));
+                            unpack2(sg, held[1].sig[i][j], held[1].sig[i][j + 1]);
+                        }
+                        if (z) {
+                            const f2 zz = pack2(rz.v[i].get(j), rz.v[i].get(j + 1)), sz = sigmoid2(zz),
+                                     gg = pack2(g[j], g[j + 1]);
+                            // (z s)' = s (1 + z (1 - s))
+                            if (!ENDS)
+                                unpack2(mul2(gg, mul2(sz, fma2(zz, fma2(sz, both2(-1.f), both2(1.f)), both2(1.f)))),
+                                        held[1].gz[i][j], held[1].gz[i][j + 1]);
+                            unpack2(mul2(gg, mul2(zz, sz)), g[j], g[j + 1]);
+                        }
                     }
-                    if (z) {
-                        float z0 = rz.v[i].get(j), z1 = rz.v[i].get(j + 1);
-                        const f2 zz = pack2(z0, z1), sz = sigmoid2(zz), gg = pack2(g[j], g[j + 1]);
-                        // (z s)' = s (1 + z (1 - s))
-                        if (!ENDS)
-                            unpack2(mul2(gg, mul2(sz, fma2(zz, fma2(sz, both2(-1.f), both2(1.f)), both2(1.f)))),
-                                    gz[i][j], gz[i][j + 1]);
-                        unpack2(mul2(gg, mul2(zz, sz)), g[j], g[j + 1]);
-                    }
+                    if (tok < L)
+#pragma unroll
+                        for (int j = 0; j < VW; ++j) {
+                            const float d = on ? dt[j] : 0.f;
+                            const f2 q[2] = {both2(d), both2(d * uf[j])};
+                            const int at = tok * CB + channel_place<Gm>(vch + j);
+                            sts_quad(in + at * 4, q);
+                            *reinterpret_cast<f2*>(in + Sh::dy + at * 2) = both2(on ? g[j] : 0.f);
+                        }
                 }
-                if (tok < L)
-#pragma unroll
-                    for (int j = 0; j < VW; ++j) {
-                        const float d = on ? dt[j] : 0.f;
-                        const f2 q[2] = {both2(d), both2(d * uf[j])};
-                        const int at = tok * CB + channel_place<Gm>(vch + j);
-                        sts_quad(in + at * 4, q);
-                        *reinterpret_cast<f2*>(in + Sh::dy + at * 2) = both2(on ? g[j] : 0.f);
-                    }
+                States::stage(w + kStates, in + Sh::B, ht, true);
             }
-            rb.stage(in + Sh::B, ht);
+            fetch(s + 2);
         };
         auto put_out = [&](int s) {
             const float* in = sm + (s & 1) * Sh::in;
@@ -280,7 +302,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                 const int tok = Rows::token(i, ht), t = t0 + tok;
                 if (tok >= L || t >= tl.t1 || vch >= tl.kleft) continue;
                 float uf[VW], du[VW], dd[VW], dz[VW];
-                raw_floats(uf, held_u[0].v[i]);
+                raw_floats(uf, held[0].u.v[i]);
 #pragma unroll
                 for (int j = 0; j < VW; ++j) {
                     const int at = tok * CB + channel_place<Gm>(vch + j);
@@ -288,8 +310,8 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                     const float gB = sum_states<Gm>(o + Sh::kSum + at * NQ);
                     const float sd = sum_states<Gm>(o + 2 * Sh::kSum + at * NQ) * kLn2;
                     du[j] = fmaf(dt, gB, skip[j] * dyh);
-                    dd[j] = fmaf(uf[j], gB, sd) * held_sig[i][j];
-                    if (z) dz[j] = held_gz[i][j] * fmaf(skip[j], uf[j], sum_states<Gm>(o + at * NQ));
+                    dd[j] = fmaf(uf[j], gB, sd) * held[0].sig[i][j];
+                    if (z) dz[j] = held[0].gz[i][j] * fmaf(skip[j], uf[j], sum_states<Gm>(o + at * NQ));
                     if (t >= tl.n) du[j] = dd[j] = dz[j] = 0.f;
                     dD[j] = fmaf(dyh, uf[j], dD[j]);
                     db[j] += dd[j];
@@ -325,36 +347,13 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                 if (ht % F == 0 && t < tl.n) sts_quad(bcp + (size_t)t * a.G * (2 * NP) + (row & 1) * NP + e % NS * 4, v);
             }
         };
-        auto hold = [&]() {
-            held_u[0] = held_u[1];
-            held_u[1] = ru;
-        };
-        float sig1[Rows::NV][VW], gz1[Rows::NV][VW];  // of the segment being walked
-        auto hold_factors = [&]() {
-#pragma unroll
-            for (int i = 0; i < Rows::NV; ++i)
-#pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    held_sig[i][j] = sig1[i][j];
-                    held_gz[i][j] = gz1[i][j];
-                    sig1[i][j] = sig[i][j];
-                    gz1[i][j] = gz[i][j];
-                }
-        };
         fetch(0);
-        stage(0);
-        hold();
-        if (!ENDS) hold_factors();
         fetch(1);
+        stage(0);
         __syncthreads();
         for (int s = 0; s <= steps; ++s) {
-            if (!ENDS && s > 0) put_out(s - 1);
+            if (!ENDS && s > 0) put_out(s - 1);  // first: it reads the buffer that is staged next
             stage(s + 1);
-            if (!ENDS) {
-                hold();
-                hold_factors();
-            }
-            fetch(s + 2);
             __syncthreads();
         }
         if constexpr (!ENDS) {
@@ -453,7 +452,7 @@ ScanBwdLayout scan_bwd_layout(int B, int T, int D, int N, int G, int chunks) {
 template <typename T, typename TG, int NS, bool ENDS>
 static cudaError_t launch_bwd_geom(const ScanArgs& a, int B, cudaStream_t st) {
     using Gm = ScanBwdGeom<NS>;
-    constexpr size_t smem = ScanBwdShared<Gm>::total * sizeof(float);
+    constexpr size_t smem = ScanBwdShared<T, TG, Gm>::total * sizeof(float);
     static_assert(smem <= 227 * 1024, "shared memory of a block");
     auto kern = scan_bwd_kernel<T, TG, Gm, ENDS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -174,29 +174,74 @@ __device__ __forceinline__ void store_states(float* p, const f2 (&s)[Gm::CH][2],
     }
 }
 
+// A helper thread's own slots in shared memory for the rows on their way, two
+// steps of them: asynchronous copies complete in order, so a step waits for its
+// own rows only. (Two sets of registers did not serve: a wait for the older
+// loads waited for the newer ones too.) RawVec<T, V> per vector; vec: the
+// address is aligned to the vector.
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+template <typename T, int V>
+__device__ __forceinline__ void slot_fetch(uint32_t* slot, const T* p, bool on, int left, int vec) {
+    using Raw = RawVec<T, V>;
+    if (on && vec) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(slot)), "l"(p), "n"(V * (int)sizeof(T))
+                     : "memory");
+        return;
+    }
+    Raw r;
+    r.zero();
+    if (on)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j < left) r.set(j, p[j]);
+#pragma unroll
+    for (int i = 0; i < Raw::kWords; ++i) slot[i] = r.w[i];
+}
+template <typename T, int V> __device__ __forceinline__ RawVec<T, V> slot_read(const uint32_t* slot) {
+    RawVec<T, V> r;
+    if constexpr (RawVec<T, V>::kWords == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(slot);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    } else if constexpr (RawVec<T, V>::kWords == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(slot);
+        r.w[0] = v.x; r.w[1] = v.y;
+    } else {
+        r.w[0] = slot[0];
+    }
+    return r;
+}
+
 // [L tokens][CB channels] of one input among the helpers: vector i of thread
 // `ht` is number v = 128 i + ht, token v / VPT, channels from (v % VPT) VW (the
 // same for every i). Tokens from n on and channels beyond the tile are not read
 // and give 0.
 template <typename T, typename Gm, int L> struct TokenRows {
-    static constexpr int VW = Gm::VW, VPT = Gm::VPT;
-    static constexpr int NV = L * VPT > kHelperThreads ? L * VPT / kHelperThreads : 1;
+    static constexpr int VW = Gm::VW, VPT = Gm::VPT, kAll = L * VPT;
+    static constexpr int NV = kAll > kHelperThreads ? kAll / kHelperThreads : 1;
+    static constexpr int kVec = RawVec<T, VW>::kWords;
+    static constexpr int kWords = (kAll < kHelperThreads ? kAll : NV * kHelperThreads) * kVec;  // of a step's slots
     RawVec<T, VW> v[NV];
     static __device__ __forceinline__ int token(int i, int ht) { return (kHelperThreads * i + ht) / VPT; }
     static __device__ __forceinline__ int channel(int ht) { return ht % VPT * VW; }
-    __device__ __forceinline__ void fetch(const T* p, long long st, int t0, const ScanTile& tl, int vec, int ht) {
+    static __device__ __forceinline__ void fetch(uint32_t* slots, const T* p, long long st, int t0, const ScanTile& tl,
+                                                 int vec, int ht) {
         const int ch = channel(ht);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int tok = token(i, ht);
-            v[i].zero();
-            if (tok >= L || t0 + tok >= tl.n || ch >= tl.kleft) continue;
-            const T* q = p + (t0 + tok) * st + ch;
-            if (vec) v[i].load(q);
-            else
+            if (tok >= L) continue;
+            slot_fetch<T, VW>(slots + (kHelperThreads * i + ht) * kVec, p + (t0 + tok) * st + ch,
+                              t0 + tok < tl.n && ch < tl.kleft, tl.kleft - ch, vec);
+        }
+    }
+    __device__ __forceinline__ void read(const uint32_t* slots, int ht) {
 #pragma unroll
-                for (int j = 0; j < VW; ++j)
-                    if (ch + j < tl.kleft) v[i].set(j, q[j]);
+        for (int i = 0; i < NV; ++i) {
+            v[i].zero();
+            if (token(i, ht) < L) v[i] = slot_read<T, VW>(slots + (kHelperThreads * i + ht) * kVec);
         }
     }
 };
@@ -210,30 +255,28 @@ template <typename T, int VW> __device__ __forceinline__ void store_row(T* p, co
 
 // [L tokens][N states] of B and of C behind it, staged as fp32 rows of NP.
 template <typename T, typename Gm, int L> struct StateRows {
-    static constexpr int kEach = L * Gm::NS, NV = 2 * kEach > kHelperThreads ? 2 * kEach / kHelperThreads : 1;
-    RawVec<T, 4> v[NV];
-    __device__ __forceinline__ void fetch(const T* Bp, const T* Cp, const ScanArgs& a, int t0, const ScanTile& tl,
-                                          int ht) {
+    static constexpr int kEach = L * Gm::NS, kAll = 2 * kEach;
+    static constexpr int NV = kAll > kHelperThreads ? kAll / kHelperThreads : 1;
+    static constexpr int kVec = RawVec<T, 4>::kWords;
+    static constexpr int kWords = (kAll < kHelperThreads ? kAll : NV * kHelperThreads) * kVec;
+    static __device__ __forceinline__ void fetch(uint32_t* slots, const T* Bp, const T* Cp, const ScanArgs& a, int t0,
+                                                 const ScanTile& tl, int ht) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = kHelperThreads * i + ht, r = e % kEach, tok = r / Gm::NS, n0 = r % Gm::NS * 4;
             const T* p = e < kEach ? Bp : Cp;
-            v[i].zero();
-            if (e >= 2 * kEach || !p || t0 + tok >= tl.n || n0 >= a.N) continue;
-            const T* q = p + (t0 + tok) * (e < kEach ? a.bs[1] : a.cs[1]) + n0;
-            if (a.bc_vec) v[i].load(q);
-            else
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (n0 + j < a.N) v[i].set(j, q[j]);
+            if (e >= kAll || !p) continue;
+            slot_fetch<T, 4>(slots + e * kVec, p + (t0 + tok) * (e < kEach ? a.bs[1] : a.cs[1]) + n0,
+                             t0 + tok < tl.n && n0 < a.N, a.N - n0, a.bc_vec);
         }
     }
-    __device__ __forceinline__ void stage(float* s, int ht) const {
+    static __device__ __forceinline__ void stage(const uint32_t* slots, float* s, int ht, bool with_c) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = kHelperThreads * i + ht;
-            if (e >= 2 * kEach) continue;
-            const f2 q[2] = {pack2(v[i].get(0), v[i].get(1)), pack2(v[i].get(2), v[i].get(3))};
+            if (e >= (with_c ? kAll : kEach)) continue;
+            const RawVec<T, 4> v = slot_read<T, 4>(slots + e * kVec);
+            const f2 q[2] = {pack2(v.get(0), v.get(1)), pack2(v.get(2), v.get(3))};
             sts_quad(s + 4 * e, q);
         }
     }
