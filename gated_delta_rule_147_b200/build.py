@@ -89,7 +89,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     link = [_nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", LIB, *[_obj(s) for s in SOURCES]]
     subprocess.run(link, check=True)
     libs = ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
-    subprocess.run([cxx, "-shared", "-o", MODULE, _obj(BINDING), LIB, "-L", os.path.join(torch_dir, "lib"), *libs,
+    # by name, found beside the module: an absolute path would tie it to this folder
+    subprocess.run([cxx, "-shared", "-o", MODULE, _obj(BINDING), "-L", HERE, "-l:libgdr.so", "-L",
+                    os.path.join(torch_dir, "lib"), *libs,
                     "-Wl,-rpath,$ORIGIN"], check=True)
     return LIB
 
