@@ -28,8 +28,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 template <typename T, typename TG, typename Gm> struct ScanBwdShared {
     static constexpr int L = Gm::Seg;
-    // floats of a step: (dt, dt u) quads, dyh pairs, B, C
-    static constexpr int dy = 4 * L * Gm::CB, B = dy + 2 * L * Gm::CB, in = B + 2 * L * Gm::NP;
+    // floats of a step: (dt, dt u) quads, dyh (twice where two blocks per SM leave
+    // the room: a pair as the walkers need it), B, C
+    static constexpr int kDup = sizeof(T) == 2 ? 2 : 1;
+    static constexpr int dy = 4 * L * Gm::CB, B = dy + kDup * L * Gm::CB, in = B + 2 * L * Gm::NP;
     // of its results: sums of C h, g B and A a g h over the states, terms of dB and dC
     static constexpr int kSum = L * Gm::CB * Gm::NQ, bc = 3 * kSum, out = bc + L * 2 * kWalkers * 128;
     // of rows on their way: delta, u, z; dy; B and C
@@ -37,7 +39,8 @@ template <typename T, typename TG, typename Gm> struct ScanBwdShared {
     using Grads = TokenRows<TG, Gm, L>;
     using States = StateRows<T, Gm, L>;
     static constexpr int slots = 3 * Rows::kWords + Grads::kWords + States::kWords;
-    static constexpr int total = 2 * (in + out + slots);
+    // and the state before each walker's next segment
+    static constexpr int ckpt = 2 * (in + out + slots), total = ckpt + kWalkers * Gm::QUADS;
 };
 
 // ENDS: the chunk's maps only, its segments in order.
@@ -50,6 +53,10 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
     const ScanTile tl(a, CB);
     const int steps = (tl.n - tl.t0 + L - 1) / L;
     float* const results = sm + 2 * Sh::in;
+    auto pair_at = [](const float* p, int at) {
+        if constexpr (Sh::kDup == 2) return *reinterpret_cast<const f2*>(p + 2 * at);
+        else return both2(p[at]);
+    };
     auto segment = [&](int s) { return ENDS ? s : steps - 1 - s; };  // of step s
     float* const prm = a.prm + ((size_t)tl.b * a.chunks + tl.part) * a.D_ * (a.N + 2);
 
@@ -80,7 +87,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                             const int at = t * CB + c * CL + at0;
                             f2 d[2];
                             lds_quad(d, in + at * 4);
-                            const f2 dyh = *reinterpret_cast<const f2*>(in + Sh::dy + at * 2);
+                            const f2 dyh = pair_at(in + Sh::dy, at);
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 const f2 e = ex2_pair(mul2(d[0], A[c][k]));
@@ -96,16 +103,20 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
             store_map<Gm>(a.ends, p, h, a, tl, warp, lane);
             store_map<Gm>(a.grad_ends, p, E, a, tl, warp, lane);
         } else {
-            f2 dA[CH][2], g[CH][2], next[CH][2];
+            f2 dA[CH][2], g[CH][2];
             load_given<Gm>(g, a.dh_T, a, tl, at0, nl);
             fold_chunks<Gm>(g, a.grad_ends, a, tl, warp, lane, a.chunks - 1, tl.part, -1);
 #pragma unroll
             for (int c = 0; c < CH; ++c) dA[c][0] = dA[c][1] = both2(0.f);
             const float* ckpt = a.ckpt + ((tl.unit * kWalkers + warp) * a.segs + tl.t0 / L) * Gm::QUADS + lane * 4;
+            float* const before = sm + Sh::ckpt + warp * Gm::QUADS + lane * 4;  // a lane's own quads
             auto fetch = [&](int s) {
-                if (s >= steps) return;
+                if (s < steps)
 #pragma unroll
-                for (int c = 0; c < CH; ++c) lds_quad(next[c], ckpt + (size_t)segment(s) * Gm::QUADS + c * 128);
+                    for (int c = 0; c < CH; ++c)
+                        slot_fetch<float, 4>(reinterpret_cast<uint32_t*>(before + c * 128),
+                                             ckpt + (size_t)segment(s) * Gm::QUADS + c * 128, true, 4, 1);
+                copies_commit();
             };
             fetch(0);
             __syncthreads();
@@ -114,12 +125,9 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                     const float* in = sm + (s & 1) * Sh::in;
                     float* o = results + (s & 1) * Sh::out;
                     f2 h0[CH][2], h[L][CH][2], dec[L][CH][2];
+                    copies_wait<0>();
 #pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        h0[c][0] = next[c][0];
-                        h0[c][1] = next[c][1];
-                    }
-                    fetch(s + 1);
+                    for (int c = 0; c < CH; ++c) lds_quad(h0[c], before + c * 128);
 #pragma unroll
                     for (int t = 0; t < L; ++t) {
                         f2 B[2];
@@ -135,6 +143,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                             }
                         }
                     }
+                    fetch(s + 1);  // h0 has been used
                     // a token's operands are loaded before the last one's sums are
                     // stored: the compiler cannot tell that the two do not overlap
                     struct { f2 B[2], C[2], d[CH][2], dyh[CH]; } x, next;  // d: dt, dt u
@@ -145,7 +154,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                         for (int c = 0; c < CH; ++c) {
                             const int at = t * CB + c * CL + at0;
                             lds_quad(v.d[c], in + at * 4);
-                            v.dyh[c] = *reinterpret_cast<const f2*>(in + Sh::dy + at * 2);
+                            v.dyh[c] = pair_at(in + Sh::dy, at);
                         }
                     };
                     load(x, L - 1);
@@ -239,87 +248,92 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
             }
             copies_commit();
         };
-        auto stage = [&](int s) {
+        // A step is one stretch of code without branches, so that the chains of the
+        // rows coming in and of the sums going out fill each other's waits.
+        Rows rd, rz;
+        Grads rg;
+        auto read = [&](int s) {
+            const uint32_t* w = slots + (s & 1) * Sh::slots;
             held[0] = held[1];
             copies_wait<1>();
-            if (s < steps) {
-                float* in = sm + (s & 1) * Sh::in;
-                const uint32_t* w = slots + (s & 1) * Sh::slots;
-                Rows rd, rz;
-                Grads rg;
-                rd.read(w, ht);
-                held[1].u.read(w + Rows::kWords, ht);
-                if (z) rz.read(w + 2 * Rows::kWords, ht);
-                rg.read(w + kGrads, ht);
-#pragma unroll
-                for (int i = 0; i < Rows::NV; ++i) {
-                    const int tok = Rows::token(i, ht);
-                    const bool on = tl.t0 + segment(s) * L + tok < tl.n && vch < tl.kleft;
-                    float raw[VW], uf[VW], dt[VW], g[VW];
-                    raw_floats(raw, rd.v[i]);
-                    raw_floats(uf, held[1].u.v[i]);
-                    raw_floats(g, rg.v[i]);
-#pragma unroll
-                    for (int j = 0; j < VW; ++j) raw[j] += bias[j];
-                    step_sizes(dt, raw, a.softplus);
-#pragma unroll
-                    for (int j = 0; j < VW; j += 2) {
-                        if (!ENDS) {
-                            f2 sg = both2(1.f);
-                            if (a.softplus) sg = sigmoid2(pack2(raw[j], raw[j + 1]));
-                            unpack2(sg, held[1].sig[i][j], held[1].sig[i][j + 1]);
-                        }
-                        if (z) {
-                            const f2 zz = pack2(rz.v[i].get(j), rz.v[i].get(j + 1)), sz = sigmoid2(zz),
-                                     gg = pack2(g[j], g[j + 1]);
-                            // (z s)' = s (1 + z (1 - s))
-                            if (!ENDS)
-                                unpack2(mul2(gg, mul2(sz, fma2(zz, fma2(sz, both2(-1.f), both2(1.f)), both2(1.f)))),
-                                        held[1].gz[i][j], held[1].gz[i][j + 1]);
-                            unpack2(mul2(gg, mul2(zz, sz)), g[j], g[j + 1]);
-                        }
-                    }
-                    if (tok < L)
-#pragma unroll
-                        for (int j = 0; j < VW; ++j) {
-                            const float d = on ? dt[j] : 0.f;
-                            const f2 q[2] = {both2(d), both2(d * uf[j])};
-                            const int at = tok * CB + channel_place<Gm>(vch + j);
-                            sts_quad(in + at * 4, q);
-                            *reinterpret_cast<f2*>(in + Sh::dy + at * 2) = both2(on ? g[j] : 0.f);
-                        }
-                }
-                States::stage(w + kStates, in + Sh::B, ht, true);
-            }
-            fetch(s + 2);
+            rd.read(w, ht);
+            held[1].u.read(w + Rows::kWords, ht);
+            rz.read(w + 2 * Rows::kWords, ht);  // not used without z
+            rg.read(w + kGrads, ht);
         };
-        auto put_out = [&](int s) {
+        auto stage = [&](int s) {  // beyond the last step into a buffer that nobody reads
+            float* in = sm + (s & 1) * Sh::in;
+            const uint32_t* w = slots + (s & 1) * Sh::slots;
+#pragma unroll
+            for (int i = 0; i < Rows::NV; ++i) {
+                const int tok = Rows::token(i, ht);
+                const bool on = tl.t0 + segment(s) * L + tok < tl.n && vch < tl.kleft;
+                float raw[VW], uf[VW], dt[VW], g[VW];
+                raw_floats(raw, rd.v[i]);
+                raw_floats(uf, held[1].u.v[i]);
+                raw_floats(g, rg.v[i]);
+#pragma unroll
+                for (int j = 0; j < VW; ++j) raw[j] += bias[j];
+                step_sizes(dt, raw, a.softplus);
+#pragma unroll
+                for (int j = 0; j < VW; j += 2) {
+                    if (!ENDS) {
+                        f2 sg = both2(1.f);
+                        if (a.softplus) sg = sigmoid2(pack2(raw[j], raw[j + 1]));
+                        unpack2(sg, held[1].sig[i][j], held[1].sig[i][j + 1]);
+                    }
+                    if (z) {
+                        const f2 zz = pack2(rz.v[i].get(j), rz.v[i].get(j + 1)), sz = sigmoid2(zz),
+                                 gg = pack2(g[j], g[j + 1]);
+                        // (z s)' = s (1 + z (1 - s))
+                        if (!ENDS)
+                            unpack2(mul2(gg, mul2(sz, fma2(zz, fma2(sz, both2(-1.f), both2(1.f)), both2(1.f)))),
+                                    held[1].gz[i][j], held[1].gz[i][j + 1]);
+                        unpack2(mul2(gg, mul2(zz, sz)), g[j], g[j + 1]);
+                    }
+                }
+                if (tok < L)
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) {
+                        const float d = on ? dt[j] : 0.f, gy = on ? g[j] : 0.f;
+                        const f2 q[2] = {both2(d), both2(d * uf[j])};
+                        const int at = tok * CB + channel_place<Gm>(vch + j);
+                        sts_quad(in + at * 4, q);
+                        if constexpr (Sh::kDup == 2) *reinterpret_cast<f2*>(in + Sh::dy + at * 2) = both2(gy);
+                        else in[Sh::dy + at] = gy;
+                    }
+            }
+            States::stage(w + kStates, in + Sh::B, ht, true);
+        };
+        auto put_out = [&](int s, const Held& h) {
             const float* in = sm + (s & 1) * Sh::in;
             const float* o = results + (s & 1) * Sh::out;
             const int t0 = tl.t0 + segment(s) * L;
 #pragma unroll
             for (int i = 0; i < Rows::NV; ++i) {
-                const int tok = Rows::token(i, ht), t = t0 + tok;
-                if (tok >= L || t >= tl.t1 || vch >= tl.kleft) continue;
+                const int tok = Rows::token(i, ht) % L, t = t0 + tok;  // % L: threads beyond the rows repeat some
+                const bool live = Rows::token(i, ht) < L && t < tl.t1 && vch < tl.kleft, on = live && t < tl.n;
                 float uf[VW], du[VW], dd[VW], dz[VW];
-                raw_floats(uf, held[0].u.v[i]);
+                raw_floats(uf, h.u.v[i]);
 #pragma unroll
                 for (int j = 0; j < VW; ++j) {
                     const int at = tok * CB + channel_place<Gm>(vch + j);
-                    const float dt = in[at * 4], dyh = in[Sh::dy + at * 2];
+                    const float dt = in[at * 4], dyh = in[Sh::dy + at * Sh::kDup];
                     const float gB = sum_states<Gm>(o + Sh::kSum + at * NQ);
                     const float sd = sum_states<Gm>(o + 2 * Sh::kSum + at * NQ) * kLn2;
                     du[j] = fmaf(dt, gB, skip[j] * dyh);
-                    dd[j] = fmaf(uf[j], gB, sd) * held[0].sig[i][j];
-                    if (z) dz[j] = held[0].gz[i][j] * fmaf(skip[j], uf[j], sum_states<Gm>(o + at * NQ));
-                    if (t >= tl.n) du[j] = dd[j] = dz[j] = 0.f;
-                    dD[j] = fmaf(dyh, uf[j], dD[j]);
+                    dd[j] = fmaf(uf[j], gB, sd) * h.sig[i][j];
+                    dz[j] = z ? h.gz[i][j] * fmaf(skip[j], uf[j], sum_states<Gm>(o + at * NQ)) : 0.f;
+                    if (!on) du[j] = dd[j] = dz[j] = 0.f;
+                    dD[j] = on ? fmaf(dyh, uf[j], dD[j]) : dD[j];
                     db[j] += dd[j];
                 }
                 const size_t row = rbase + (size_t)t * a.D_;
-                store_row(a.du + row, du, tl.kleft - vch, a.act_vec);
-                store_row(a.ddelta + row, dd, tl.kleft - vch, a.act_vec);
-                if (z) store_row(a.dz + row, dz, tl.kleft - vch, a.act_vec);
+                if (live) {
+                    store_row(a.du + row, du, tl.kleft - vch, a.act_vec);
+                    store_row(a.ddelta + row, dd, tl.kleft - vch, a.act_vec);
+                    if (z) store_row(a.dz + row, dz, tl.kleft - vch, a.act_vec);
+                }
             }
             // dB, dC over the block's channels: quad e is token e / (2 NS), B or C, 4
             // states; F threads add up to 4 CL terms, each row from another lane on
@@ -347,13 +361,23 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                 if (ht % F == 0 && t < tl.n) sts_quad(bcp + (size_t)t * a.G * (2 * NP) + (row & 1) * NP + e % NS * 4, v);
             }
         };
+        auto bring_in = [&](int s) {
+            read(s);
+            stage(s);
+            fetch(s + 2);
+        };
         fetch(0);
         fetch(1);
-        stage(0);
+        bring_in(0);
         __syncthreads();
-        for (int s = 0; s <= steps; ++s) {
-            if (!ENDS && s > 0) put_out(s - 1);  // first: it reads the buffer that is staged next
+        bring_in(1);
+        __syncthreads();
+        for (int s = 1; s <= steps; ++s) {
+            const Held last = held[0];
+            read(s + 1);
+            if (!ENDS) put_out(s - 1, last);  // before the staging: it reads the buffer that is staged next
             stage(s + 1);
+            fetch(s + 2 + 1);
             __syncthreads();
         }
         if constexpr (!ENDS) {
