@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
                         for (int c = 0; c < CH; ++c) {
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
-                                h[c][k] = fma2(ex2_pair(mul2(x.d[c][0], A[c][k])), h[c][k], mul2(x.d[c][1], x.B[k]));
+                                h[c][k] = fma2(decay2(x.d[c][0], A[c][k]), h[c][k], mul2(x.d[c][1], x.B[k]));
                             if (MODE == kScanEnds) total[c] = add2(total[c], x.d[c][0]);
                             if (MODE == kScanOut) {
                                 const float v = fold_states<Gm>(sum2(fma2(x.C[1], h[c][1], mul2(x.C[0], h[c][0]))));
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
                     raw_floats(uf, held_u[1].v[i]);
 #pragma unroll
                     for (int j = 0; j < VW; ++j) raw[j] += bias[j];
-                    step_sizes(dt, raw, a.softplus);
+                    step_sizes<false>(dt, dt, raw, a.softplus);
                     if (tok < LT)
 #pragma unroll
                         for (int j = 0; j < VW; ++j) {
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(256, kStepBlocks) scan_step_kernel(ScanArgs a,
             for (int i = 0; i < 4; ++i) A[k][i] = fmaxf(A[k][i] * kLog2e, -3.402823466e38f);  // as load_states
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                f2 v = fma2(ex2_pair(mul2(both2(dtc), pack2(A[k][2 * q], A[k][2 * q + 1]))),
+                f2 v = fma2(decay2(both2(dtc), pack2(A[k][2 * q], A[k][2 * q + 1])),
                             pack2(s[k][2 * q], s[k][2 * q + 1]), mul2(both2(dtu), B[q]));
                 yv = fma2(C[q], v, yv);
                 unpack2(v, s[k][2 * q], s[k][2 * q + 1]);

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                             const f2 dyh = pair_at(in + Sh::dy, at);
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const f2 e = ex2_pair(mul2(d[0], A[c][k]));
+                                const f2 e = decay2(d[0], A[c][k]);
                                 h[c][k] = fma2(e, h[c][k], mul2(d[1], B[k]));
                                 p[c][k] = mul2(p[c][k], e);
                                 E[c][k] = fma2(p[c][k], mul2(C[k], dyh), E[c][k]);
@@ -103,11 +103,11 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
             store_map<Gm>(a.ends, p, h, a, tl, warp, lane);
             store_map<Gm>(a.grad_ends, p, E, a, tl, warp, lane);
         } else {
-            f2 dA[CH][2], g[CH][2];
+            f2 dA[CH][2], lost[CH][2], g[CH][2];  // dA: a compensated sum of the segments'
             load_given<Gm>(g, a.dh_T, a, tl, at0, nl);
             fold_chunks<Gm>(g, a.grad_ends, a, tl, warp, lane, a.chunks - 1, tl.part, -1);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) dA[c][0] = dA[c][1] = both2(0.f);
+            for (int c = 0; c < CH; ++c) dA[c][0] = dA[c][1] = lost[c][0] = lost[c][1] = both2(0.f);
             const float* ckpt = a.ckpt + ((tl.unit * kWalkers + warp) * a.segs + tl.t0 / L) * Gm::QUADS + lane * 4;
             float* const before = sm + Sh::ckpt + warp * Gm::QUADS + lane * 4;  // a lane's own quads
             auto fetch = [&](int s) {
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                             lds_quad(d, in + (t * CB + c * CL + at0) * 4);
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                dec[t][c][k] = ex2_pair(mul2(d[0], A[c][k]));
+                                dec[t][c][k] = decay2(d[0], A[c][k]);
                                 h[t][c][k] = fma2(dec[t][c][k], t == 0 ? h0[c][k] : h[t - 1][c][k], mul2(d[1], B[k]));
                             }
                         }
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                         }
                     };
                     load(x, L - 1);
+                    f2 part[CH][2];
 #pragma unroll
                     for (int t = L - 1; t >= 0; --t) {
                         if (t > 0) load(next, t - 1);
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                                 dC[k] = c == 0 ? mul2(ht, x.dyh[c]) : fma2(ht, x.dyh[c], dC[k]);
                                 g[c][k] = mul2(dec[t][c][k], gt);
                                 const f2 w = mul2(g[c][k], t == 0 ? h0[c][k] : h[t - 1][c][k]);
-                                dA[c][k] = fma2(w, x.d[c][0], dA[c][k]);
+                                part[c][k] = t == L - 1 ? mul2(w, x.d[c][0]) : fma2(w, x.d[c][0], part[c][k]);
                                 dd = k == 0 ? mul2(A[c][k], w) : fma2(A[c][k], w, dd);  // A log2(e) here
                             }
                             vy[c] = fold_states<Gm>(sum2(yc));
@@ -195,6 +196,15 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                         sts_quad(o + Sh::bc + ((2 * t + 1) * kWalkers + warp) * 128 + lane * 4, dC);
                         x = next;
                     }
+                    const f2 minus = both2(-1.f);
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const f2 v = fma2(lost[c][k], minus, part[c][k]), sum = add2(dA[c][k], v);
+                            lost[c][k] = fma2(v, minus, fma2(dA[c][k], minus, sum));
+                            dA[c][k] = sum;
+                        }
                 }
                 __syncthreads();
             }
@@ -274,14 +284,9 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                 raw_floats(g, rg.v[i]);
 #pragma unroll
                 for (int j = 0; j < VW; ++j) raw[j] += bias[j];
-                step_sizes(dt, raw, a.softplus);
+                step_sizes<!ENDS>(dt, held[1].sig[i], raw, a.softplus);
 #pragma unroll
                 for (int j = 0; j < VW; j += 2) {
-                    if (!ENDS) {
-                        f2 sg = both2(1.f);
-                        if (a.softplus) sg = sigmoid2(pack2(raw[j], raw[j + 1]));
-                        unpack2(sg, held[1].sig[i][j], held[1].sig[i][j + 1]);
-                    }
                     if (z) {
                         const f2 zz = pack2(rz.v[i].get(j), rz.v[i].get(j + 1)), sz = sigmoid2(zz),
                                  gg = pack2(g[j], g[j + 1]);

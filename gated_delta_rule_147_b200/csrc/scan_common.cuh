@@ -286,13 +286,15 @@ template <typename T, int VW> __device__ __forceinline__ void raw_floats(float (
 #pragma unroll
     for (int i = 0; i < VW; ++i) f[i] = r.get(i);
 }
-// dt of raw steps.
-template <int VW> __device__ __forceinline__ void step_sizes(float (&dt)[VW], const float (&raw)[VW], int softplus) {
+// dt of raw steps, and (SIG) its derivative.
+template <bool SIG, int VW>
+__device__ __forceinline__ void step_sizes(float (&dt)[VW], float (&sig)[VW], const float (&raw)[VW], int softplus) {
 #pragma unroll
     for (int i = 0; i < VW; i += 2) {
-        dt[i] = raw[i];
-        dt[i + 1] = raw[i + 1];
-        if (softplus) unpack2(softplus2(pack2(raw[i], raw[i + 1])), dt[i], dt[i + 1]);
+        StepCurve c = {pack2(raw[i], raw[i + 1]), both2(1.f)};
+        if (softplus) c = softplus2<SIG>(c.dt);
+        unpack2(c.dt, dt[i], dt[i + 1]);
+        if (SIG) unpack2(c.sig, sig[i], sig[i + 1]);
     }
 }
 // Channels' values from a [D] array, 0 where absent.
