@@ -28,6 +28,17 @@ template <typename T, typename Gm> struct ScanFwdShared {
     static constexpr int slots = 3 * Rows::kWords + States::kWords, total = 2 * (in + out + slots);
 };
 
+// Where a split forward chunk's fold starts: the first launch goes through chunk
+// 0 from h0 itself and leaves h0 in the place of that chunk's decay, so that the
+// second launch, which writes h_T (it may be h0), does not read h0.
+template <typename Gm>
+__device__ __forceinline__ void load_first(f2 (&s)[Gm::CH][2], const ScanArgs& a, const ScanTile& tl, int walker,
+                                           int lane) {
+    const float* p = a.ends + (tl.unit * a.chunks * kWalkers + walker) * 2 * Gm::QUADS + lane * 4;
+#pragma unroll
+    for (int c = 0; c < Gm::CH; ++c) lds_quad(s[c], p + (tl.part ? Gm::QUADS : 0) + c * 128);
+}
+
 template <typename T, typename Gm, int MODE>
 __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * kFwdBlocks) scan_fwd_kernel(ScanArgs a) {
     constexpr int CH = Gm::CH, LT = Gm::LT, CB = Gm::CB, CL = Gm::CL, NP = Gm::NP;
@@ -44,8 +55,20 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
         const int nl = lane % Gm::NS, cl = lane / Gm::NS, p0 = lane_place<Gm>(warp, 0, cl);
         f2 A[CH][2], h[CH][2];
         load_states<Gm>(A, a.A, tl, a.N, a.state_vec, p0, nl, kLog2e, true);
-        load_given<Gm>(h, MODE == kScanEnds ? nullptr : a.h0, a, tl, p0, nl);
-        if (MODE != kScanEnds) fold_chunks<Gm>(h, a.ends, a, tl, warp, lane, 0, tl.part, 1);
+        if (MODE == kScanOut && a.chunks > 1) {
+            load_first<Gm>(h, a, tl, warp, lane);
+            fold_chunks<Gm>(h, a.ends, a, tl, warp, lane, 1, tl.part, 1);
+        } else {
+            load_given<Gm>(h, MODE == kScanEnds && tl.part ? nullptr : a.h0, a, tl, p0, nl);
+            if (MODE == kScanCkpt) fold_chunks<Gm>(h, a.ends, a, tl, warp, lane, 0, tl.part, 1);
+        }
+        f2 first[CH][2];
+        if (MODE == kScanEnds)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                first[c][0] = h[c][0];
+                first[c][1] = h[c][1];
+            }
         f2 total[CH];  // sum of dt
         if (MODE == kScanEnds)
 #pragma unroll
@@ -101,7 +124,7 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) p[c][k] = ex2_pair(mul2(total[c], A[c][k]));
+                for (int k = 0; k < 2; ++k) p[c][k] = tl.part ? ex2_pair(mul2(total[c], A[c][k])) : first[c][k];
             store_map<Gm>(a.ends, p, h, a, tl, warp, lane);
         }
         const int last = max(seq_len(a.lengths, tl.b, a.T) - 1, 0) / a.chunk;

@@ -328,7 +328,7 @@ template <typename Gm> __device__ __forceinline__ float sum_states(const float* 
 template <typename Gm>
 __device__ __forceinline__ void fold_chunks(f2 (&s)[Gm::CH][2], const float* ends, const ScanArgs& a,
                                             const ScanTile& tl, int walker, int lane, int from, int to, int step) {
-    for (int c = from; c != to; c += step) {
+    for (int c = from; step > 0 ? c < to : c > to; c += step) {
         const float* p = ends + ((tl.unit * a.chunks + c) * kWalkers + walker) * 2 * Gm::QUADS + lane * 4;
 #pragma unroll
         for (int i = 0; i < Gm::CH; ++i) {

@@ -203,6 +203,11 @@ def test_scan_split_workspace(cuda_device):
         got[name] = gdr.scan_fwd(*args, workspace=ws, **kw)
         check_scan(dict(zip(("y", "h_T"), got[name])), ref, ("y", "h_T"))
     assert torch.equal(got["none"][0], got["small"][0]) and torch.equal(got["none"][1], got["small"][1])
+    for n in (None, torch.tensor([700], dtype=torch.int32, device=cuda_device)):  # the state carried in place
+        want = gdr.scan_fwd(*args, lengths=n, **kw)
+        h = i["h0"].clone()
+        y, h_T = gdr.scan_fwd(*args[:-1], h, h_T=h, lengths=n, **kw)
+        assert h_T is h and torch.equal(h, want[1]) and torch.equal(y, want[0])
 
 
 @pytest.mark.parametrize("dtype,D,N,G", [(BF, 48, 16, 1), (F32, 10, 7, 2), (BF, 4, 128, 1), (F32, 33, 4, 1)])
