@@ -21,8 +21,9 @@
 namespace gdr {
 
 // Channels of a thread and tokens of a batch. Forward, 2 x 4096 x 8192 bf16, 4
-// taps: 4 channels and 4 tokens 56.6 us, 4 and 8 63.8, 8 and 4 60.7. Backward,
-// 4 x 4096 x 6144: 4 and 4 172 us, 4 and 2 199, 2 and 4 207.
+// taps: 4 channels and 4 tokens 56.6 us (4.7 TB/s), 4 and 8 63.8, 8 and 4 60.7.
+// Backward, 4 x 4096 x 6144: 4 and 4 164 us (4.9 TB/s), 4 and 2 about 190, 2 and 4
+// about 200.
 constexpr int kConvVec = 4, kConvAhead = 4;
 
 struct ConvShape {
@@ -355,60 +356,70 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(const float* __restric
     }
 }
 
-template <typename T, int V, int W, bool VEC>
+// SEQ sequences of V channels per thread: with several, the taps are read once
+// for all of them and more rows are on their way.
+template <typename T, int V, int W, bool VEC, int SEQ>
 __global__ void __launch_bounds__(128) conv_step_kernel(const T* __restrict__ x, const void* __restrict__ weight,
                                                         const void* __restrict__ bias, T* __restrict__ X,
-                                                        T* __restrict__ y, long long xb, ConvShape s) {
+                                                        T* __restrict__ y, long long xb, int B, ConvShape s) {
     constexpr int P = V / 2;
     using Row = RowIO<T, V, VEC>;
     dependent_launch();
     const unsigned idx = blockIdx.x * 128u + threadIdx.x;
     if (idx >= s.total) return;
-    const int b = idx / s.nvec;
-    const int c = (idx - b * s.nvec) * V, left = s.D - c;
+    const int b0 = idx / s.nvec;
+    const int c = (idx - b0 * s.nvec) * V, left = s.D - c;
     f2 w[W][P], bs[P];
-    Row rows[W];
+    Row rows[SEQ][W];
     dependent_wait();
-    T* Xr = X + (size_t)b * (W - 1) * s.D + c;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) rows[j].load(Xr + (size_t)j * s.D, left);
-    rows[W - 1].load(x + b * xb + c, left);
-    load_taps<T, V, W, VEC>(w, bs, weight, bias, c, left, s.w_f32);
-    f2 out[P];
+    for (int q = 0; q < SEQ; ++q) {
+        const int b = b0 * SEQ + q;
+        if (b >= B) continue;
+        const T* Xr = X + (size_t)b * (W - 1) * s.D + c;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        out[i] = bs[i];
-#pragma unroll
-        for (int j = 0; j < W; ++j) out[i] = fma2(w[j][i], rows[j].pair(i), out[i]);
-        if (s.silu) out[i] = mul2(out[i], sigmoid2(out[i]));
+        for (int j = 0; j < W - 1; ++j) rows[q][j].load(Xr + (size_t)j * s.D, left);
+        rows[q][W - 1].load(x + b * xb + c, left);
     }
-    Row::store(y + (size_t)b * s.D + c, out, left);
+    load_taps<T, V, W, VEC>(w, bs, weight, bias, c, left, s.w_f32);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        f2 f[P];
+    for (int q = 0; q < SEQ; ++q) {
+        const int b = b0 * SEQ + q;
+        if (b >= B) continue;
+        f2 out[P];
 #pragma unroll
-        for (int i = 0; i < P; ++i) f[i] = rows[j + 1].pair(i);
-        Row::store(Xr + (size_t)j * s.D, f, left);
+        for (int i = 0; i < P; ++i) {
+            out[i] = bs[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) out[i] = fma2(w[j][i], rows[q][j].pair(i), out[i]);
+            if (s.silu) out[i] = mul2(out[i], sigmoid2(out[i]));
+        }
+        Row::store(y + (size_t)b * s.D + c, out, left);
+        T* Xr = X + (size_t)b * (W - 1) * s.D + c;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            f2 f[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) f[i] = rows[q][j + 1].pair(i);
+            Row::store(Xr + (size_t)j * s.D, f, left);
+        }
     }
 }
 
 // Tokens per thread. A chunk of tt tokens loads W - 1 halo rows and writes one
-// set of partials, so longer is better (forward of the case above: 32 tokens
-// 59.7 us, 64 and 128 56.6; backward: 64 tokens 188 us, 128 184, 256 172) until
-// there are too few threads to keep the loads in flight; `want` threads fill
-// the card.
-static int conv_tokens(long long per_token, int T, int lo, int hi, long long want) {
-    int tt = hi;
-    while (tt > lo && per_token * ((T + tt - 1) / tt) < want) tt /= 2;
-    return tt;
+// set of partials, so longer is better, up to `hi`; but the threads should come
+// to a whole number of waves of `wave` threads (two here), and to enough of them
+// that the loads stay in flight. Backward of the case above: 256 tokens make 1.7
+// waves and take 171 us.
+static int conv_tokens(long long per_token, int T, int lo, int hi, long long wave) {
+    const long long chunks = 2 * wave / per_token;
+    long long tt = chunks > 0 ? (T + chunks - 1) / chunks : hi;
+    tt = (tt + kConvAhead - 1) / kConvAhead * kConvAhead;
+    return (int)(tt < lo ? lo : tt > hi ? hi : tt);
 }
-
-static int conv_fwd_tokens(int B, int T, int nvec) {
-    return conv_tokens((long long)B * nvec, T, 8, 64, 148 * 1024);
-}
-static int conv_bwd_tokens(int B, int T, int nvec) {
-    return conv_tokens((long long)B * nvec, T, 16, 256, 148 * 512);
-}
+// Resident threads: 7 blocks of 128 (70 registers) and 3 (162) to an SM.
+static int conv_fwd_tokens(int B, int T, int nvec) { return conv_tokens((long long)B * nvec, T, 8, 64, 148 * 7 * 128); }
+static int conv_bwd_tokens(int B, int T, int nvec) { return conv_tokens((long long)B * nvec, T, 16, 256, 148 * 3 * 128); }
 static int conv_vectors(int D) { return (D + kConvVec - 1) / kConvVec; }
 static int conv_chunks(int T, int tt) { return T > 0 ? (T + tt - 1) / tt : 1; }
 
@@ -565,7 +576,9 @@ gdr_status gdr_conv_step(const void* x, const void* weight, const void* bias, vo
     s.T = 1; s.D = D; s.nvec = conv_vectors(D);
     s.silu = activation == GDR_ACT_SILU;
     s.w_f32 = weight_dtype == GDR_FP32;
-    const long long total = (long long)B * s.nvec;
+    // four sequences a thread while that leaves two waves of threads or so
+    const bool several = (long long)B * s.nvec >= 4ll * 148 * 1024;
+    const long long total = (long long)(several ? (B + 3) / 4 : B) * s.nvec;
     if (total > (1ll << 31)) return GDR_ERR_UNSUPPORTED;
     s.total = (unsigned)total;
     const unsigned grid = (unsigned)((total + 127) / 128);
@@ -573,9 +586,11 @@ gdr_status gdr_conv_step(const void* x, const void* weight, const void* bias, vo
     cudaError_t err = cudaErrorInvalidValue;
     dispatch_taps(W, [&](auto wc) {
         constexpr int WT = decltype(wc)::value;
-#define GDR_CONV_STEP(TT, VEC)                                                                      \
-    err = launch_dependent(conv_step_kernel<TT, kConvVec, WT, VEC>, grid, 128, 0, st, (const TT*)x, weight,    \
-                           bias, (TT*)X, (TT*)y, xb, s)
+#define GDR_CONV_STEP(TT, VEC)                                                                                     \
+    err = several ? launch_dependent(conv_step_kernel<TT, kConvVec, WT, VEC, 4>, grid, 128, 0, st, (const TT*)x, weight, \
+                                     bias, (TT*)X, (TT*)y, xb, B, s)                                               \
+                  : launch_dependent(conv_step_kernel<TT, kConvVec, WT, VEC, 1>, grid, 128, 0, st, (const TT*)x, weight, \
+                                     bias, (TT*)X, (TT*)y, xb, B, s)
         if (dtype == GDR_BF16) {
             if (vec) GDR_CONV_STEP(__nv_bfloat16, true); else GDR_CONV_STEP(__nv_bfloat16, false);
         } else {

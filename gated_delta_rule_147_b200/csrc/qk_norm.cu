@@ -31,10 +31,10 @@
 namespace gdr {
 
 // Rows a lane group requests ahead, and blocks per SM. Forward, 2 x 8192 tokens
-// of 64 heads of 128 in bf16: 4 and 3 take 95.6 us, 2 and 3 106, 2 and 4 103, 4
-// and 4 (spills) 103. Backward, 2 x 4096 tokens of 32 heads of 256: 2 and 2 take
-// 122 us, 1 and 2 135, 1 and 3 (spills) 131.
-constexpr int kFwdAhead = 4, kFwdBlocks = 3, kBwdAhead = 2, kBwdBlocks = 2;
+// of 64 heads of 128 in bf16: 4 and 3 take 95.5 us (5.6 TB/s), 2 and 3 106, 2 and
+// 4 103, 4 and 4 (spills) 103. Backward, 2 x 4096 tokens of 32 heads of 256: 3 and
+// 2 take 111 us (4.8 TB/s), 2 and 2 113, 1 and 2 135, 1 and 3 (spills) 131.
+constexpr int kFwdAhead = 4, kFwdBlocks = 3, kBwdAhead = 3, kBwdBlocks = 2;
 constexpr int kNormThreads = 256;
 constexpr int kNormMaxParts = 148 * kBwdBlocks;  // backward: one wave of blocks, each with sums of its own
 

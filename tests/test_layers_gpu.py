@@ -116,6 +116,16 @@ def test_conv_steps_continue_the_sequence(cuda_device, dtype, D, W):
     assert gdr.conv_fwd(x, w, b, X, final_state=False)[1] is None
 
 
+@pytest.mark.parametrize("dtype,B,D", [(BF, 203, 12288), (F32, 810, 2999)])
+def test_conv_step_of_a_large_batch(cuda_device, dtype, B, D):
+    """Several sequences to a thread, the last thread with fewer: the same as a
+    prompt of one token."""
+    r = Rnd(cuda_device, B)
+    x, w, b, X = r(B, D, dtype=dtype), r(D, 4, dtype=dtype), r(D, dtype=dtype), r(B, 3, D, dtype=dtype)
+    y, X_T = gdr.conv_fwd(x[:, None], w, b, X)
+    assert torch.equal(gdr.conv_step(x, w, b, X), y[:, 0]) and torch.equal(X, X_T)
+
+
 def test_conv_extremes(cuda_device):
     """Inputs whose activation saturates: no NaN, the limits of silu."""
     x = torch.tensor([1e30, -1e30, 200.0, -200.0, 0.0], device=cuda_device)[None, :, None].repeat(1, 1, 4)
