@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -209,10 +210,9 @@ struct Where {
         launch = raw ? c10::cuda::getStreamFromExternal(raw, d.index()) : c10::cuda::getDefaultCUDAStream(d.index());
     }
     Tensor empty(at::IntArrayRef shape, at::ScalarType type, bool result = true) {
-        const auto opt = at::TensorOptions().dtype(type).device(dev);
-        if (!side) return at::empty(shape, opt);
+        if (!side) return at::detail::empty_cuda(shape, type, dev, c10::nullopt);
         c10::cuda::CUDAStreamGuard guard(launch);
-        Tensor t = at::empty(shape, opt);
+        Tensor t = at::detail::empty_cuda(shape, type, dev, c10::nullopt);
         if (result) t.record_stream(here);
         return t;
     }
