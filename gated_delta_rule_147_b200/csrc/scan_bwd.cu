@@ -103,11 +103,11 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
             store_map<Gm>(a.ends, p, h, a, tl, warp, lane);
             store_map<Gm>(a.grad_ends, p, E, a, tl, warp, lane);
         } else {
-            f2 dA[CH][2], lost[CH][2], g[CH][2];  // dA: a compensated sum of the segments'
+            f2 dA[CH][2], g[CH][2];  // dA: a sum of the segments' sums, for accuracy
             load_given<Gm>(g, a.dh_T, a, tl, at0, nl);
             fold_chunks<Gm>(g, a.grad_ends, a, tl, warp, lane, a.chunks - 1, tl.part, -1);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) dA[c][0] = dA[c][1] = lost[c][0] = lost[c][1] = both2(0.f);
+            for (int c = 0; c < CH; ++c) dA[c][0] = dA[c][1] = both2(0.f);
             const float* ckpt = a.ckpt + ((tl.unit * kWalkers + warp) * a.segs + tl.t0 / L) * Gm::QUADS + lane * 4;
             float* const before = sm + Sh::ckpt + warp * Gm::QUADS + lane * 4;  // a lane's own quads
             auto fetch = [&](int s) {
@@ -196,15 +196,10 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                         sts_quad(o + Sh::bc + ((2 * t + 1) * kWalkers + warp) * 128 + lane * 4, dC);
                         x = next;
                     }
-                    const f2 minus = both2(-1.f);
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const f2 v = fma2(lost[c][k], minus, part[c][k]), sum = add2(dA[c][k], v);
-                            lost[c][k] = fma2(v, minus, fma2(dA[c][k], minus, sum));
-                            dA[c][k] = sum;
-                        }
+                        for (int k = 0; k < 2; ++k) dA[c][k] = add2(dA[c][k], part[c][k]);
                 }
                 __syncthreads();
             }
@@ -237,8 +232,8 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
         using Grads = typename Sh::Grads;
         using States = typename Sh::States;
         // what the output needs of the segments staged and walked: u, ddt/ddelta,
-        // dy dgate/dz
-        struct Held { Rows u; float sig[Rows::NV][VW], gz[Rows::NV][VW]; } held[2];
+        // dy dgate/dz, dt, dyh
+        struct Held { Rows u; float sig[Rows::NV][VW], gz[Rows::NV][VW], dt[Rows::NV][VW], dyh[Rows::NV][VW]; } held[2];
         uint32_t* const slots = reinterpret_cast<uint32_t*>(results + 2 * Sh::out);
         float bias[VW], skip[VW], dD[VW], db[VW];
 #pragma unroll
@@ -303,6 +298,8 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                         const float d = on ? dt[j] : 0.f, gy = on ? g[j] : 0.f;
                         const f2 q[2] = {both2(d), both2(d * uf[j])};
                         const int at = tok * CB + channel_place<Gm>(vch + j);
+                        held[1].dt[i][j] = d;
+                        held[1].dyh[i][j] = gy;
                         sts_quad(in + at * 4, q);
                         if constexpr (Sh::kDup == 2) *reinterpret_cast<f2*>(in + Sh::dy + at * 2) = both2(gy);
                         else in[Sh::dy + at] = gy;
@@ -311,7 +308,6 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
             States::stage(w + kStates, in + Sh::B, ht, true);
         };
         auto put_out = [&](int s, const Held& h) {
-            const float* in = sm + (s & 1) * Sh::in;
             const float* o = results + (s & 1) * Sh::out;
             const int t0 = tl.t0 + segment(s) * L;
 #pragma unroll
@@ -323,7 +319,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
 #pragma unroll
                 for (int j = 0; j < VW; ++j) {
                     const int at = tok * CB + channel_place<Gm>(vch + j);
-                    const float dt = in[at * 4], dyh = in[Sh::dy + at * Sh::kDup];
+                    const float dt = h.dt[i][j], dyh = h.dyh[i][j];
                     const float gB = sum_states<Gm>(o + Sh::kSum + at * NQ);
                     const float sd = sum_states<Gm>(o + 2 * Sh::kSum + at * NQ) * kLn2;
                     du[j] = fmaf(dt, gB, skip[j] * dyh);
@@ -380,7 +376,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
         for (int s = 1; s <= steps; ++s) {
             const Held last = held[0];
             read(s + 1);
-            if (!ENDS) put_out(s - 1, last);  // before the staging: it reads the buffer that is staged next
+            if (!ENDS) put_out(s - 1, last);
             stage(s + 1);
             fetch(s + 2 + 1);
             __syncthreads();
