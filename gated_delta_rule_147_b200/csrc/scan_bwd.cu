@@ -417,23 +417,37 @@ struct ScanReduce {
     const int* lengths;
     float *dB, *dC, *dA, *dD, *dbias;
     long long vecs;  // B * T * G
-    int T, G, D_, N, NP, tiles, parts;  // parts: sequences x chunks
+    int T, G, D_, N, NP, tiles, parts, wide;  // parts: sequences x chunks; wide: 16-byte stores
     unsigned bc_blocks;
 };
 
 __global__ void __launch_bounds__(256) scan_reduce_kernel(ScanReduce r) {
     dependent_wait();
     if (blockIdx.x < r.bc_blocks) {
+        // 4 states of one token's dB or dC per thread, eight tiles on their way
         const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
-        const long long vec = e / (2 * r.NP);
-        const int i = (int)(e - vec * (2 * r.NP)), n = i % r.NP;
+        const int quads = r.NP / 2;  // of a token's B and C
+        const long long vec = e / quads;
+        const int i = (int)(e - vec * quads) * 4, n = i % r.NP;
         if (vec >= r.vecs || n >= r.N) return;
         const long long tok = vec / r.G;
         const int b = (int)(tok / r.T), t = (int)(tok - (long long)b * r.T);
-        float s = 0.f;
-        if (t < seq_len(r.lengths, b, r.T))
-            for (int k = 0; k < r.tiles; ++k) s += r.bcpart[(size_t)k * r.vecs * (2 * r.NP) + e];
-        (i < r.NP ? r.dB : r.dC)[vec * r.N + n] = s;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        const float4* p = reinterpret_cast<const float4*>(r.bcpart) + e;
+        const size_t stride = (size_t)r.vecs * quads;
+        if (t < seq_len(r.lengths, b, r.T)) {
+#pragma unroll 8
+            for (int k = 0; k < r.tiles; ++k) {
+                const float4 v = p[k * stride];
+                s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+            }
+        }
+        float* o = (i < r.NP ? r.dB : r.dC) + vec * r.N + n;
+        if (r.wide) VecIO<float, 4>::store(o, s);
+        else
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < r.N) o[j] = s[j];
         return;
     }
     const long long e = (long long)(blockIdx.x - r.bc_blocks) * 256 + threadIdx.x;
@@ -528,7 +542,8 @@ cudaError_t launch_scan_bwd(ScanArgs a, void* ws, float* dA, float* dB, float* d
     r.vecs = (long long)B * a.T * a.G;
     r.T = a.T; r.G = a.G; r.D_ = a.D_; r.N = a.N; r.NP = 4 * scan_lanes(a.N); r.tiles = a.tiles;
     r.parts = B * a.chunks;
-    const long long bc = (r.vecs * 2 * r.NP + 255) / 256, pr = ((long long)a.D_ * (a.N + 2) + 255) / 256;
+    r.wide = a.N % 4 == 0 && aligned_to(dB, 16) && aligned_to(dC, 16);
+    const long long bc = (r.vecs * (r.NP / 2) + 255) / 256, pr = ((long long)a.D_ * (a.N + 2) + 255) / 256;
     if (bc + pr > 0x7fffffffll) return cudaErrorInvalidValue;
     r.bc_blocks = (unsigned)bc;
     return launch_dependent(scan_reduce_kernel, (unsigned)(bc + pr), 256, 0, st, r);
