@@ -20,9 +20,9 @@ enum { kScanOut = 0, kScanEnds = 1, kScanCkpt = 2 };  // y; chunk maps; states e
 
 // Words of shared memory: two steps of inputs (dt, dt u; B, C) and of sums, and
 // of rows on their way (delta, u, z; B and C).
-template <typename T, typename Gm> struct ScanFwdShared {
+template <typename T, typename Gm, bool OUT> struct ScanFwdShared {
     static constexpr int LT = Gm::LT;
-    static constexpr int in = 4 * LT * Gm::CB + 2 * LT * Gm::NP, out = LT * Gm::CB * Gm::NQ;
+    static constexpr int in = 4 * LT * Gm::CB + 2 * LT * Gm::NP, out = OUT ? LT * Gm::CB * Gm::NQ : 0;
     using Rows = TokenRows<T, Gm, LT>;
     using States = StateRows<T, Gm, LT>;
     static constexpr int slots = 3 * Rows::kWords + States::kWords, total = 2 * (in + out + slots);
@@ -42,7 +42,7 @@ __device__ __forceinline__ void load_first(f2 (&s)[Gm::CH][2], const ScanArgs& a
 template <typename T, typename Gm, int MODE>
 __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * kFwdBlocks) scan_fwd_kernel(ScanArgs a) {
     constexpr int CH = Gm::CH, LT = Gm::LT, CB = Gm::CB, CL = Gm::CL, NP = Gm::NP;
-    using Sh = ScanFwdShared<T, Gm>;
+    using Sh = ScanFwdShared<T, Gm, MODE == kScanOut>;
     constexpr int kIn = Sh::in, kOut = Sh::out;
     extern __shared__ __align__(16) float sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -236,10 +236,11 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
 }
 
 template <typename T, int NS, int MODE> static cudaError_t launch_fwd_geom(const ScanArgs& a, int B, cudaStream_t st) {
-    using Gm = std::conditional_t<MODE == kScanCkpt, ScanBwdGeom<NS>, ScanFwdGeom<NS>>;
+    using Gm = std::conditional_t<MODE == kScanCkpt, ScanCkptGeom<NS>,
+                                  std::conditional_t<MODE == kScanEnds, ScanEndsGeom<NS>, ScanFwdGeom<NS>>>;
     const long long grid = (long long)B * a.G * a.tiles * a.chunks;
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-    constexpr size_t smem = ScanFwdShared<T, Gm>::total * sizeof(float);
+    constexpr size_t smem = ScanFwdShared<T, Gm, MODE == kScanOut>::total * sizeof(float);
     static_assert(smem <= 227 * 1024, "shared memory of a block");
     auto kern = scan_fwd_kernel<T, Gm, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -270,7 +271,7 @@ int scan_chunks(int B, int T, int K, int N, int G) {
 // Sets the split; a chunk is a whole number of steps and segments.
 void scan_split(ScanArgs& a, int chunks, int CH) {
     const int per = (a.T + chunks - 1) / chunks;
-    a.chunk = per < 16 ? 16 : (per + 15) / 16 * 16;
+    a.chunk = per < 32 ? 32 : (per + 31) / 32 * 32;
     a.chunks = a.T > 0 ? (a.T + a.chunk - 1) / a.chunk : 1;
     a.tiles = scan_tiles(a.K, a.N, CH);
 }

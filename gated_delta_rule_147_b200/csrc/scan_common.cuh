@@ -58,7 +58,7 @@ struct ScanArgs {
     float *ends, *grad_ends;
 };
 
-template <int NS_, int CH_, int VW_> struct ScanGeom {
+template <int NS_, int CH_, int VW_, int STEPS_> struct ScanGeom {
     static constexpr int NS = NS_, CH = CH_;
     static constexpr int NP = 4 * NS;               // padded states
     static constexpr int CL = 32 / NS;              // channel lanes
@@ -66,7 +66,7 @@ template <int NS_, int CH_, int VW_> struct ScanGeom {
     static constexpr int CB = kWalkers * CPW;       // channels of a block
     static constexpr int NQ = NS < 4 ? NS : 4;      // partial sums over the states that go to shared memory
     static constexpr int QUADS = CH * 32 * 4;       // floats of a walker's state
-    static constexpr int LT = NS * 4 >= 8 * CH ? 16 : NS * 4 >= 4 * CH ? 8 : 4;  // tokens of a step: bounded by shared memory
+    static constexpr int LT = STEPS_ * (NS * 4 >= 8 * CH ? 16 : NS * 4 >= 4 * CH ? 8 : 4);  // tokens of a step: bounded by shared memory
     static constexpr int Seg = NS <= 2 ? 4 : 8;     // tokens of a backward segment, likewise
     // the helpers move rows in vectors of VW channels
     static constexpr int VW = VW_ < CB ? VW_ : CB, VPT = CB / VW;
@@ -76,8 +76,11 @@ template <int NS_, int CH_, int VW_> struct ScanGeom {
 // (its checkpoints too): 1 channel and 2 blocks 1130 us for 2 x 4096 x 4096 x 16
 // (ragged), 2 and 1 1325. Vectors: every helper thread has work with 16 states.
 constexpr int kFwdBlocks = 2, kBwdBlocks = 2;
-template <int NS> using ScanFwdGeom = ScanGeom<NS, 2, 4>;
-template <int NS> using ScanBwdGeom = ScanGeom<NS, 1, 2>;
+// Steps of 16 tokens with 16 states (8: 531 us), of 32 where no sums are kept.
+template <int NS> using ScanFwdGeom = ScanGeom<NS, 2, 4, 1>;
+template <int NS> using ScanEndsGeom = ScanGeom<NS, 2, 4, 2>;
+template <int NS> using ScanBwdGeom = ScanGeom<NS, 1, 2, 1>;
+template <int NS> using ScanCkptGeom = ScanGeom<NS, 1, 2, 2>;
 constexpr int scan_segment(int ns) { return ns <= 2 ? 4 : 8; }
 
 // Block -> (sequence, group, channel tile, chunk of tokens), tile fastest:
