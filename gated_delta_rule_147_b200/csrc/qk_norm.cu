@@ -447,12 +447,24 @@ static int norm_lanes(int d) {
     return l;
 }
 
-// Tokens per block: one per lane group when that still gives every SM twelve
-// blocks (four waves), fewer (several groups share a token's heads) below that.
-static int norm_tokens_per_block(long long tokens, int lanes) {
-    int tpb = kNormThreads / lanes;
-    while (tpb > 1 && (tokens + tpb - 1) / tpb < 148 * 12) tpb /= 2;
-    return tpb < 16 ? tpb : 16;
+// Tokens per block: more of them share a block's cosines, fewer (several lane
+// groups then share a token's heads) make more blocks. Least cost of waves of
+// `blocks` blocks (backward: turns of that many), each the rows of a lane group
+// and about four rows' time for the cosines: 6 x 391 tokens of 6 heads of 67
+// backward take 45 us with one token a block, 9 with eight.
+static int norm_tokens_per_block(long long tokens, int lanes, int rows, long long blocks) {
+    const int slots = kNormThreads / lanes;
+    int best = 1;
+    long long least = -1;
+    for (int tpb = slots < 16 ? slots : 16; tpb >= 1; tpb /= 2) {
+        const long long groups = (tokens + tpb - 1) / tpb, each = (rows + slots / tpb - 1) / (slots / tpb);
+        const long long cost = (groups + blocks - 1) / blocks * (4 + each);
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = tpb;
+        }
+    }
+    return best;
 }
 
 template <int L, bool VEC, typename F> static void dispatch_rot(const NormArgs& a, F&& f) {
@@ -550,7 +562,7 @@ gdr_status gdr_qk_norm_fwd(const void* q, const void* k, const void* q_weight, c
     a.q_out = q_out; a.k_out = k_out;
     const bool vec = norm_vector(a, false, e);
     const int lanes = vec ? norm_lanes(d) : 32;
-    a.tpb = norm_tokens_per_block(a.tokens, lanes);
+    a.tpb = norm_tokens_per_block(a.tokens, lanes, H_q + H_k, 148 * kFwdBlocks);
     const long long grid = (a.tokens + a.tpb - 1) / a.tpb;
     if (grid > 0x7fffffffll) return GDR_ERR_UNSUPPORTED;
     const size_t smem = (size_t)a.tpb * rot * sizeof(float);
@@ -604,7 +616,7 @@ gdr_status gdr_qk_norm_bwd(const void* q, const void* k, const void* q_weight, c
     if (T > 0) {
         const bool vec = norm_vector(a, true, eg);
         const int lanes = vec ? norm_lanes(d) : 32;
-        a.tpb = norm_tokens_per_block(a.tokens, lanes);
+        a.tpb = norm_tokens_per_block(a.tokens, lanes, H_q + H_k, kNormMaxParts);
         grid = (a.tokens + a.tpb - 1) / a.tpb;
         if (grid > kNormMaxParts) grid = kNormMaxParts;
         const size_t smem = (size_t)a.tpb * rot * sizeof(float);
