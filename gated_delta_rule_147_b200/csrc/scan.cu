@@ -150,9 +150,19 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
             uint32_t* w = slots + (s & 1) * Sh::slots;
             if (s < steps) {
                 const int t0 = tl.t0 + s * LT;
-                Rows::fetch(w, dl, a.ds[1], t0, tl, a.act_vec, ht);
-                Rows::fetch(w + Rows::kWords, u, a.us[1], t0, tl, a.act_vec, ht);
-                if (z) Rows::fetch(w + 2 * Rows::kWords, z, a.zs[1], t0, tl, a.act_vec, ht);
+                if (copies_fit<T>(a.act_vec)) {
+                    Rows::fetch(w, dl, a.ds[1], t0, tl, a.act_vec, ht);
+                    Rows::fetch(w + Rows::kWords, u, a.us[1], t0, tl, a.act_vec, ht);
+                    if (z) Rows::fetch(w + 2 * Rows::kWords, z, a.zs[1], t0, tl, a.act_vec, ht);
+                } else {
+                    Rows r[3];
+                    r[0].load(dl, a.ds[1], t0, tl, ht);
+                    r[1].load(u, a.us[1], t0, tl, ht);
+                    if (z) r[2].load(z, a.zs[1], t0, tl, ht);
+                    r[0].store(w, ht);
+                    r[1].store(w + Rows::kWords, ht);
+                    if (z) r[2].store(w + 2 * Rows::kWords, ht);
+                }
                 States::fetch(w + 3 * Rows::kWords, Bm, Cm, a, t0, tl, ht);
             }
             copies_commit();
@@ -220,7 +230,7 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
 #pragma unroll
                     for (int j = 0; j < VW; ++j)
                         if (t >= tl.n) f[j] = 0.f;
-                    store_row(y + (size_t)t * a.D_, f, tl.kleft - vch, a.act_vec);
+                    store_row(y + (size_t)t * a.D_, f, tl.kleft - vch, a.out_vec);
                 }
             }
             __syncthreads();
@@ -326,7 +336,7 @@ __global__ void __launch_bounds__(256, kStepBlocks) scan_step_kernel(ScanArgs a,
     if (mine) {
         const T* Bp = reinterpret_cast<const T*>(a.Bm) + b * a.bs[0] + g * a.N + n0;
         const T* Cp = reinterpret_cast<const T*>(a.Cm) + b * a.cs[0] + g * a.N + n0;
-        if (a.bc_vec) {
+        if (a.bc_vec == kWhole) {
             Br.load(Bp);
             Cr.load(Cp);
         } else {

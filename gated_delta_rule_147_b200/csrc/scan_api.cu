@@ -43,13 +43,20 @@ static gdr_status scan_fill(ScanArgs& a, const void* u, const void* delta, const
         a.us[i] = s[i]; a.ds[i] = s[2 + i]; a.bs[i] = s[4 + i]; a.cs[i] = s[6 + i]; a.zs[i] = s[8 + i];
         if (with_dy) a.gs[i] = s[10 + i];
     }
-    // wide accesses of 4 elements: B and C, and token rows (the caller adds its outputs)
-    a.bc_vec = N % 4 == 0 && aligned_to(Bm, 4 * e) && aligned_to(Cm, 4 * e);
-    a.act_vec = a.K % 4 == 0 && aligned_to(u, 4 * e) && aligned_to(delta, 4 * e) && aligned_to(z, 4 * e);
-    for (int i = 0; i < 2; ++i) {
-        if (a.bs[i] % 4 || a.cs[i] % 4) a.bc_vec = 0;
-        if (a.us[i] % 4 || a.ds[i] % 4 || (z && a.zs[i] % 4) || a.gs[i] % 4) a.act_vec = 0;
-    }
+    // B and C, and the token rows, in aligned vectors of 4 or pairs (dy: see gdr_scan_bwd)
+    auto bc = [&](int m) {
+        bool ok = N % m == 0 && aligned_to(Bm, m * e) && aligned_to(Cm, m * e);
+        for (int i = 0; i < 2; ++i) ok = ok && a.bs[i] % m == 0 && a.cs[i] % m == 0;
+        return ok;
+    };
+    auto rows = [&](int m) {
+        bool ok = a.K % m == 0 && aligned_to(u, m * e) && aligned_to(delta, m * e) && aligned_to(z, m * e);
+        for (int i = 0; i < 2; ++i)
+            ok = ok && a.us[i] % m == 0 && a.ds[i] % m == 0 && (!z || a.zs[i] % m == 0) && a.gs[i] % m == 0;
+        return ok;
+    };
+    a.bc_vec = bc(4) ? kWhole : bc(2) ? kPairs : kSingle;
+    a.act_vec = rows(4) ? kWhole : rows(2) ? kPairs : kSingle;
     return GDR_OK;
 }
 
@@ -81,7 +88,7 @@ gdr_status gdr_scan_fwd(const void* u, const void* delta, const float* A, const 
     if (T > 0 && !y) return GDR_ERR_INVALID_ARG;
     if (!aligned_to(y, dtype_size(dtype)) || !aligned_to(h_T, 4)) return GDR_ERR_MISALIGNED;
     a.y = y; a.h_T = h_T;
-    a.act_vec = a.act_vec && aligned_to(y, 4 * dtype_size(dtype));
+    a.out_vec = a.K % 4 == 0 && aligned_to(y, 4 * dtype_size(dtype));
     a.state_vec = states_in_quads(N, {A, h0, h_T});
     if (workspace && !aligned_to(workspace, 256)) return GDR_ERR_MISALIGNED;
     const size_t need = gdr_scan_fwd_workspace_size(B, T, D_, N, G);
@@ -120,8 +127,10 @@ gdr_status gdr_scan_bwd(const void* u, const void* delta, const float* A, const 
         if (!aligned_to(p, 4)) return GDR_ERR_MISALIGNED;
     a.dy = dy; a.dh_T = dh_T;
     a.du = du; a.ddelta = ddelta; a.dz = dz; a.dh0 = dh0;
-    a.act_vec = a.act_vec && aligned_to(dy, 4 * dtype_size(grad_dtype)) && aligned_to(du, 16) &&
-                aligned_to(ddelta, 16) && aligned_to(dz, 16);
+    const size_t eg = dtype_size(grad_dtype);
+    if (a.act_vec == kWhole && !aligned_to(dy, 4 * eg)) a.act_vec = kPairs;
+    if (a.act_vec == kPairs && !aligned_to(dy, 2 * eg)) a.act_vec = kSingle;
+    a.out_vec = a.K % 4 == 0 && aligned_to(du, 16) && aligned_to(ddelta, 16) && aligned_to(dz, 16);
     a.state_vec = states_in_quads(N, {A, h0, dh_T, dh0});
     return launched(launch_scan_bwd(a, workspace, dA, dB, dC, dD, ddelta_bias, B, dtype, grad_dtype,
                                     reinterpret_cast<cudaStream_t>(stream)));

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
                         slot_fetch<float, 4>(reinterpret_cast<uint32_t*>(before + c * 128),
-                                             ckpt + (size_t)segment(s) * Gm::QUADS + c * 128, true, 4, 1);
+                                             ckpt + (size_t)segment(s) * Gm::QUADS + c * 128, true, 4, kWhole);
                 copies_commit();
             };
             fetch(0);
@@ -245,10 +245,23 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
             uint32_t* w = slots + (s & 1) * Sh::slots;
             if (s < steps) {
                 const int t0 = tl.t0 + segment(s) * L;
-                Rows::fetch(w, dl, a.ds[1], t0, tl, a.act_vec, ht);
-                Rows::fetch(w + Rows::kWords, u, a.us[1], t0, tl, a.act_vec, ht);
-                if (z) Rows::fetch(w + 2 * Rows::kWords, z, a.zs[1], t0, tl, a.act_vec, ht);
-                Grads::fetch(w + kGrads, dy, a.gs[1], t0, tl, a.act_vec, ht);
+                if (copies_fit<T>(a.act_vec)) {
+                    Rows::fetch(w, dl, a.ds[1], t0, tl, a.act_vec, ht);
+                    Rows::fetch(w + Rows::kWords, u, a.us[1], t0, tl, a.act_vec, ht);
+                    if (z) Rows::fetch(w + 2 * Rows::kWords, z, a.zs[1], t0, tl, a.act_vec, ht);
+                    Grads::fetch(w + kGrads, dy, a.gs[1], t0, tl, a.act_vec, ht);
+                } else {
+                    Rows r[3];
+                    Grads g;
+                    r[0].load(dl, a.ds[1], t0, tl, ht);
+                    r[1].load(u, a.us[1], t0, tl, ht);
+                    if (z) r[2].load(z, a.zs[1], t0, tl, ht);
+                    g.load(dy, a.gs[1], t0, tl, ht);
+                    r[0].store(w, ht);
+                    r[1].store(w + Rows::kWords, ht);
+                    if (z) r[2].store(w + 2 * Rows::kWords, ht);
+                    g.store(w + kGrads, ht);
+                }
                 States::fetch(w + kStates, Bm, Cm, a, t0, tl, ht);
             }
             copies_commit();
@@ -331,9 +344,9 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                 }
                 const size_t row = rbase + (size_t)t * a.D_;
                 if (live) {
-                    store_row(a.du + row, du, tl.kleft - vch, a.act_vec);
-                    store_row(a.ddelta + row, dd, tl.kleft - vch, a.act_vec);
-                    if (z) store_row(a.dz + row, dz, tl.kleft - vch, a.act_vec);
+                    store_row(a.du + row, du, tl.kleft - vch, a.out_vec);
+                    store_row(a.ddelta + row, dd, tl.kleft - vch, a.out_vec);
+                    if (z) store_row(a.dz + row, dz, tl.kleft - vch, a.out_vec);
                 }
             }
             // dB, dC over the block's channels: quad e is token e / (2 NS), B or C, 4

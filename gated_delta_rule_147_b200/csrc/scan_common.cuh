@@ -45,7 +45,8 @@ struct ScanArgs {
     float* h_T;
     long long us[2], ds[2], bs[2], cs[2], zs[2], gs[2];  // batch and token strides
     int T, D_, N, G, K, tiles, softplus;
-    int state_vec, bc_vec, act_vec;  // wide accesses: states, B and C, token rows
+    int state_vec, out_vec;  // 16-byte state accesses, wide stores of output rows
+    int bc_vec, act_vec;     // alignment of B and C, and of the token rows (kSingle, kWhole, kPairs)
     // backward
     const float* dh_T;
     float *du, *ddelta, *dz, *dh0;
@@ -180,28 +181,44 @@ __device__ __forceinline__ void store_states(float* p, const f2 (&s)[Gm::CH][2],
 // A helper thread's own slots in shared memory for the rows on their way, two
 // steps of them: asynchronous copies complete in order, so a step waits for its
 // own rows only. (Two sets of registers did not serve: a wait for the older
-// loads waited for the newer ones too.) RawVec<T, V> per vector; vec: the
-// address is aligned to the vector.
+// loads waited for the newer ones too.) A RawVec<T, V> per vector.
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT> __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
+// vec: kWhole vectors or kPairs of elements are aligned to their size, or only
+// elements are. Copies are of 4 bytes at least, so single bf16 elements take
+// plain loads (slot_load, then slot_store once all loads of a step are under way).
+enum { kSingle = 0, kWhole = 1, kPairs = 2 };
+template <typename T> __device__ __forceinline__ bool copies_fit(int vec) { return sizeof(T) == 4 || vec != kSingle; }
+
 template <typename T, int V>
 __device__ __forceinline__ void slot_fetch(uint32_t* slot, const T* p, bool on, int left, int vec) {
-    using Raw = RawVec<T, V>;
-    if (on && vec) {
+    if (on && vec == kWhole) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(slot)), "l"(p), "n"(V * (int)sizeof(T))
                      : "memory");
         return;
     }
-    Raw r;
+    constexpr int kPer = 4 / sizeof(T);  // elements of a word
+#pragma unroll
+    for (int i = 0; i < RawVec<T, V>::kWords; ++i) {
+        if (on && i * kPer < left)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(slot + i)), "l"(p + i * kPer)
+                         : "memory");
+        else slot[i] = 0;
+    }
+}
+template <typename T, int V> __device__ __forceinline__ RawVec<T, V> slot_load(const T* p, bool on, int left) {
+    RawVec<T, V> r;
     r.zero();
-    if (on)
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (j < left) r.set(j, p[j]);
+    for (int j = 0; j < V; ++j)
+        if (on && j < left) r.set(j, p[j]);
+    return r;
+}
+template <typename T, int V> __device__ __forceinline__ void slot_store(uint32_t* slot, const RawVec<T, V>& r) {
 #pragma unroll
-    for (int i = 0; i < Raw::kWords; ++i) slot[i] = r.w[i];
+    for (int i = 0; i < RawVec<T, V>::kWords; ++i) slot[i] = r.w[i];
 }
 template <typename T, int V> __device__ __forceinline__ RawVec<T, V> slot_read(const uint32_t* slot) {
     RawVec<T, V> r;
@@ -240,6 +257,20 @@ template <typename T, typename Gm, int L> struct TokenRows {
                               t0 + tok < tl.n && ch < tl.kleft, tl.kleft - ch, vec);
         }
     }
+    // the same with plain loads: first all inputs' loads, then the stores
+    __device__ __forceinline__ void load(const T* p, long long st, int t0, const ScanTile& tl, int ht) {
+        const int ch = channel(ht);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int tok = token(i, ht);
+            v[i] = slot_load<T, VW>(p + (t0 + tok) * st + ch, tok < L && t0 + tok < tl.n && ch < tl.kleft, tl.kleft - ch);
+        }
+    }
+    __device__ __forceinline__ void store(uint32_t* slots, int ht) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (token(i, ht) < L) slot_store<T, VW>(slots + (kHelperThreads * i + ht) * kVec, v[i]);
+    }
     __device__ __forceinline__ void read(const uint32_t* slots, int ht) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -262,15 +293,36 @@ template <typename T, typename Gm, int L> struct StateRows {
     static constexpr int NV = kAll > kHelperThreads ? kAll / kHelperThreads : 1;
     static constexpr int kVec = RawVec<T, 4>::kWords;
     static constexpr int kWords = (kAll < kHelperThreads ? kAll : NV * kHelperThreads) * kVec;
+    // vector i of a thread: where it is read from (null: nowhere) and how many states are left
+    struct Source { const T* p; bool any, on; int left; };
+    static __device__ __forceinline__ Source source(int i, const T* Bp, const T* Cp, const ScanArgs& a, int t0,
+                                                    const ScanTile& tl, int ht) {
+        const int e = kHelperThreads * i + ht, r = e % kEach, tok = r / Gm::NS, n0 = r % Gm::NS * 4;
+        const T* p = e < kEach ? Bp : Cp;
+        return {p + (t0 + tok) * (e < kEach ? a.bs[1] : a.cs[1]) + n0, e < kAll && p, t0 + tok < tl.n && n0 < a.N, a.N - n0};
+    }
     static __device__ __forceinline__ void fetch(uint32_t* slots, const T* Bp, const T* Cp, const ScanArgs& a, int t0,
                                                  const ScanTile& tl, int ht) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = kHelperThreads * i + ht, r = e % kEach, tok = r / Gm::NS, n0 = r % Gm::NS * 4;
-            const T* p = e < kEach ? Bp : Cp;
-            if (e >= kAll || !p) continue;
-            slot_fetch<T, 4>(slots + e * kVec, p + (t0 + tok) * (e < kEach ? a.bs[1] : a.cs[1]) + n0,
-                             t0 + tok < tl.n && n0 < a.N, a.N - n0, a.bc_vec);
+            const Source s = source(i, Bp, Cp, a, t0, tl, ht);
+            uint32_t* slot = slots + (kHelperThreads * i + ht) * kVec;
+            if (s.any && copies_fit<T>(a.bc_vec)) slot_fetch<T, 4>(slot, s.p, s.on, s.left, a.bc_vec);
+        }
+        if (copies_fit<T>(a.bc_vec)) return;
+        constexpr int kTogether = NV < 4 ? NV : 4;
+#pragma unroll
+        for (int i0 = 0; i0 < NV; i0 += kTogether) {
+            RawVec<T, 4> v[kTogether];
+#pragma unroll
+            for (int i = 0; i < kTogether; ++i) {
+                const Source s = source(i0 + i, Bp, Cp, a, t0, tl, ht);
+                v[i] = slot_load<T, 4>(s.p, s.any && s.on, s.left);
+            }
+#pragma unroll
+            for (int i = 0; i < kTogether; ++i)
+                if (source(i0 + i, Bp, Cp, a, t0, tl, ht).any)
+                    slot_store<T, 4>(slots + (kHelperThreads * (i0 + i) + ht) * kVec, v[i]);
         }
     }
     static __device__ __forceinline__ void stage(const uint32_t* slots, float* s, int ht, bool with_c) {
