@@ -50,7 +50,9 @@ struct NormArgs {
     float eps, q_scale, rscale, inv_d, inv_eps;
 };
 
-enum { kHalf = 1, kInterleaved = 2 };  // ROT: layout of the rotation, 0 for none
+// ROT: layout of the rotation, 0 for none. kHalfShared: partners that do not lie
+// in whole vectors (rot not a multiple of 16) go through shared memory.
+enum { kHalf = 1, kInterleaved = 2, kHalfShared = 3 };
 
 // Sequence and position in it of a token.
 __device__ __forceinline__ void token_of(const NormArgs& a, long long tok, long long& b, long long& t) {
@@ -84,12 +86,12 @@ __device__ __forceinline__ void fill_turns(const NormArgs& a, long long tok0, fl
     }
 }
 
-// One lane's 8 elements of a row: e(i) = 8 li + i (VEC), or li + 32 i.
-template <bool VEC> __device__ __forceinline__ int row_elem(int li, int i) { return VEC ? 8 * li + i : li + 32 * i; }
+// One lane's 8 elements of a row: e(i) = 8 li + i (VEC), or li + L i.
+template <int L, bool VEC> __device__ __forceinline__ int row_elem(int li, int i) { return VEC ? 8 * li + i : li + L * i; }
 
 // The elements as loaded, and as numbers. A lane's elements from d on are
 // never loaded and stay 0; a row that is not wanted keeps what it held.
-template <typename T, bool VEC> struct LaneRow {
+template <typename T, int L, bool VEC> struct LaneRow {
     RawVec<T, 8> v;
     __device__ __forceinline__ void load(const T* row, int li, int d, bool on) {
         if constexpr (VEC) {
@@ -98,7 +100,7 @@ template <typename T, bool VEC> struct LaneRow {
             if (on) v.zero();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (on && li + 32 * i < d) v.set(i, row[32 * i]);
+                if (on && li + L * i < d) v.set(i, row[L * i]);
         }
     }
     __device__ __forceinline__ void get(f2 (&f)[4]) const {
@@ -106,7 +108,7 @@ template <typename T, bool VEC> struct LaneRow {
         for (int i = 0; i < 4; ++i) f[i] = pack2(v.get(2 * i), v.get(2 * i + 1));
     }
 };
-template <typename T, bool VEC>
+template <typename T, int L, bool VEC>
 __device__ __forceinline__ void store_lane(T* row, const f2 (&v)[4], int li, int d) {
     float f[8];
 #pragma unroll
@@ -116,7 +118,7 @@ __device__ __forceinline__ void store_lane(T* row, const f2 (&v)[4], int li, int
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (li + 32 * i < d) row[32 * i] = from_f32<T>(f[i]);
+            if (li + L * i < d) row[L * i] = from_f32<T>(f[i]);
     }
 }
 
@@ -129,13 +131,13 @@ template <typename T> __device__ __forceinline__ void fill_weights(float* sw, co
         sw[(i < a.d ? 0 : 256) + e] = i < a.d ? w * q_scale : w;
     }
 }
-template <bool VEC> __device__ __forceinline__ void lane_weight(f2 (&w)[4], const float* sw, int li) {
+template <int L, bool VEC> __device__ __forceinline__ void lane_weight(f2 (&w)[4], const float* sw, int li) {
     float f[8];
     if constexpr (VEC) {
         VecIO<float, 8>::load(f, sw + 8 * li);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = sw[li + 32 * i];
+        for (int i = 0; i < 8; ++i) f[i] = sw[li + L * i];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = pack2(f[2 * i], f[2 * i + 1]);
@@ -149,14 +151,14 @@ template <int L> __device__ __forceinline__ float row_sum(float v) {
 
 // c, s of a lane's elements: out = y c + partner s (s carries the sign, and
 // another for the transposed rotation: sign = -1); 1 and 0 where not rotated.
-template <bool VEC, int ROT>
+template <int L, bool VEC, int ROT>
 __device__ __forceinline__ void lane_turns(f2 (&c)[4], f2 (&s)[4], const NormArgs& a, const float* cs, const float* sn,
                                            int li, float sign) {
     const int half = a.rot / 2;
     float cf[8], sf[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int e = row_elem<VEC>(li, i);
+        const int e = row_elem<L, VEC>(li, i);
         cf[i] = 1.f;
         sf[i] = 0.f;
         if (e < a.rot) {
@@ -174,8 +176,8 @@ __device__ __forceinline__ void lane_turns(f2 (&c)[4], f2 (&s)[4], const NormArg
 }
 
 // Turns a lane's elements in place. src: the lane of the half layout's
-// partners (its own where not rotated). buf: this warp's row in shared memory
-// (plain form only).
+// partners (its own where not rotated). buf: the lane group's row in shared
+// memory (kHalfShared and the plain form).
 template <int L, bool VEC, int ROT>
 __device__ __forceinline__ void rotate(f2 (&y)[4], const f2 (&c)[4], const f2 (&s)[4], const NormArgs& a, int li,
                                        int src, float* buf) {
@@ -185,18 +187,22 @@ __device__ __forceinline__ void rotate(f2 (&y)[4], const f2 (&c)[4], const f2 (&
     if constexpr (VEC && ROT == kInterleaved) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = f[i ^ 1];
-    } else if constexpr (VEC) {
+    } else if constexpr (VEC && ROT == kHalf) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, f[i], src, L);
     } else {
         const int half = a.rot / 2;
         __syncwarp();
+        if constexpr (VEC) {
+            VecIO<float, 8>::store(buf + 8 * li, f);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) buf[li + 32 * i] = f[i];
+            for (int i = 0; i < 8; ++i) buf[li + L * i] = f[i];
+        }
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int e = li + 32 * i;
+            const int e = row_elem<L, VEC>(li, i);
             o[i] = e < a.rot ? buf[ROT == kInterleaved ? e ^ 1 : (e < half ? e + half : e - half)] : 0.f;
         }
     }
@@ -247,11 +253,12 @@ __device__ __forceinline__ HeadRows<T> output_rows(void* q, void* k, long long t
 template <typename T, int L, bool VEC, int ROT>
 __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(NormArgs a) {
     extern __shared__ float sm[];
-    __shared__ float rowbuf[VEC ? 1 : kNormThreads / 32][VEC ? 1 : 256];
+    constexpr bool kBuf = !VEC || ROT == kHalfShared;
+    __shared__ __align__(16) float rowbuf[kBuf ? kNormThreads / L : 1][kBuf ? 8 * L : 1];
     __shared__ __align__(16) float sw[512];
     constexpr int kSlots = kNormThreads / L, kAhead = sizeof(T) == 2 ? kFwdAhead : kFwdAhead / 2;
     float *cs = sm, *sn = sm + a.tpb * (a.rot / 2);
-    const int li = threadIdx.x % L, slot = threadIdx.x / L, e0 = row_elem<VEC>(li, 0);
+    const int li = threadIdx.x % L, slot = threadIdx.x / L, e0 = row_elem<L, VEC>(li, 0);
     const int spt = kSlots / a.tpb;  // lane groups that share a token
     const long long tok0 = (long long)blockIdx.x * a.tpb, tok = tok0 + slot / spt;
     const int R = a.Hq + a.Hk, h0 = slot % spt, src = partner_lane(a, li);
@@ -263,7 +270,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(N
     const auto out = output_rows<T>(a.q_out, a.k_out, tok, a.Hq, a.Hk, a.d, e0);
     dependent_launch();
     dependent_wait();
-    LaneRow<T, VEC> row[kAhead];
+    LaneRow<T, L, VEC> row[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
         row[j].v.zero();
@@ -273,8 +280,8 @@ __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(N
     if (ROT) fill_turns(a, tok0, cs, sn);
     if (weighted || ROT) __syncthreads();
     f2 c[4], s[4];
-    if (ROT) lane_turns<VEC, ROT>(c, s, a, cs + (slot / spt) * (a.rot / 2), sn + (slot / spt) * (a.rot / 2), li, 1.f);
-    float* buf = rowbuf[VEC ? 0 : slot];
+    if (ROT) lane_turns<L, VEC, ROT>(c, s, a, cs + (slot / spt) * (a.rot / 2), sn + (slot / spt) * (a.rot / 2), li, 1.f);
+    float* buf = rowbuf[kBuf ? slot : 0];
     // every lane of a warp runs the same number of rows: shuffles need them all
     for (int hb = 0; hb < R; hb += kAhead * spt) {
 #pragma unroll
@@ -290,7 +297,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(N
             float r = row_rnorm(a, row_sum<L>(sum2(sq)), &inside);
             if (weighted) {
                 f2 w[4];
-                lane_weight<VEC>(w, sw + (h < a.Hq ? 0 : 256), li);
+                lane_weight<L, VEC>(w, sw + (h < a.Hq ? 0 : 256), li);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], mul2(both2(r), w[i]));
             } else {
@@ -299,7 +306,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(N
                 for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], both2(r));
             }
             if constexpr (ROT != 0) rotate<L, VEC, ROT>(y, c, s, a, li, src, buf);
-            if (h < last) store_lane<T, VEC>(out.at(h), y, li, a.d);
+            if (h < last) store_lane<T, L, VEC>(out.at(h), y, li, a.d);
         }
     }
 }
@@ -307,11 +314,12 @@ __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(N
 template <typename T, typename TG, int L, bool VEC, int ROT>
 __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(NormArgs a) {
     extern __shared__ float sm[];
-    __shared__ float rowbuf[VEC ? 1 : kNormThreads / 32][VEC ? 1 : 256];
+    constexpr bool kBuf = !VEC || ROT == kHalfShared;
+    __shared__ __align__(16) float rowbuf[kBuf ? kNormThreads / L : 1][kBuf ? 8 * L : 1];
     __shared__ __align__(16) float sw[512];
     constexpr int kSlots = kNormThreads / L, kAhead = sizeof(T) == 2 ? kBwdAhead : 1;
     float *cs = sm, *sn = sm + a.tpb * (a.rot / 2);
-    const int li = threadIdx.x % L, slot = threadIdx.x / L, e0 = row_elem<VEC>(li, 0);
+    const int li = threadIdx.x % L, slot = threadIdx.x / L, e0 = row_elem<L, VEC>(li, 0);
     const int spt = kSlots / a.tpb;
     const int R = a.Hq + a.Hk, h0 = slot % spt, src = partner_lane(a, li);
     const bool weighted = a.qw || a.kw;
@@ -319,9 +327,9 @@ __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(N
 #pragma unroll
     for (int i = 0; i < 4; ++i) dqw[i] = dkw[i] = both2(0.f);
     if (weighted) fill_weights<T>(sw, a, 1.f);
-    float* buf = rowbuf[VEC ? 0 : slot];
-    LaneRow<T, VEC> xrow[kAhead];
-    LaneRow<TG, VEC> grow[kAhead];
+    float* buf = rowbuf[kBuf ? slot : 0];
+    LaneRow<T, L, VEC> xrow[kAhead];
+    LaneRow<TG, L, VEC> grow[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
         xrow[j].v.zero();
@@ -347,7 +355,7 @@ __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(N
         if (ROT) {
             fill_turns(a, tok0, cs, sn);
             __syncthreads();
-            lane_turns<VEC, ROT>(c, s, a, cs + (slot / spt) * (a.rot / 2), sn + (slot / spt) * (a.rot / 2), li, -1.f);
+            lane_turns<L, VEC, ROT>(c, s, a, cs + (slot / spt) * (a.rot / 2), sn + (slot / spt) * (a.rot / 2), li, -1.f);
         }
         for (int hb = 0; hb < R; hb += kAhead * spt) {
 #pragma unroll
@@ -361,7 +369,7 @@ __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(N
                 grow[j].load(gin.at(ahead), li, a.d, ahead < last);
                 if constexpr (ROT != 0) rotate<L, VEC, ROT>(g, c, s, a, li, src, buf);
                 if (weighted) {
-                    lane_weight<VEC>(gw, sw + (isq ? 0 : 256), li);
+                    lane_weight<L, VEC>(gw, sw + (isq ? 0 : 256), li);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) gw[i] = mul2(gw[i], g[i]);
                 } else {
@@ -393,7 +401,7 @@ __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(N
 #pragma unroll
                         for (int i = 0; i < 4; ++i) dkw[i] = fma2(g[i], x[i], dkw[i]);
                     }
-                    store_lane<float, VEC>(out.at(h), dx, li, a.d);
+                    store_lane<float, L, VEC>(out.at(h), dx, li, a.d);
                 }
             }
         }
@@ -408,8 +416,8 @@ __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(N
         for (int i = 0; i < 4; ++i) {
             float lo, hi;
             unpack2(which ? dkw[i] : mul2(dqw[i], both2(a.q_scale)), lo, hi);
-            red[slot][row_elem<VEC>(li, 2 * i)] = lo;
-            red[slot][row_elem<VEC>(li, 2 * i + 1)] = hi;
+            red[slot][row_elem<L, VEC>(li, 2 * i)] = lo;
+            red[slot][row_elem<L, VEC>(li, 2 * i + 1)] = hi;
         }
         __syncthreads();
         for (int e = threadIdx.x; e < a.d; e += kNormThreads) {
@@ -440,7 +448,7 @@ __global__ void __launch_bounds__(256) qk_norm_reduce_kernel(const float* __rest
     }
 }
 
-// Lanes of a row: a power of two that covers d / 8 vectors; 32 in the plain form.
+// Lanes of a row: a power of two that covers d / 8.
 static int norm_lanes(int d) {
     int l = 2;
     while (l * 8 < d) l *= 2;
@@ -472,16 +480,16 @@ template <int L, bool VEC, typename F> static void dispatch_rot(const NormArgs& 
     using VC = std::integral_constant<bool, VEC>;
     if (!a.rot) f(LC(), VC(), std::integral_constant<int, 0>());
     else if (a.interleaved) f(LC(), VC(), std::integral_constant<int, kInterleaved>());
+    else if (VEC && a.rot % 16) f(LC(), VC(), std::integral_constant<int, VEC ? kHalfShared : kHalf>());
     else f(LC(), VC(), std::integral_constant<int, kHalf>());
 }
 template <typename F> static void dispatch_lanes(const NormArgs& a, bool vec, int lanes, F&& f) {
-    if (!vec) { dispatch_rot<32, false>(a, f); return; }
     switch (lanes) {
-        case 2: dispatch_rot<2, true>(a, f); break;
-        case 4: dispatch_rot<4, true>(a, f); break;
-        case 8: dispatch_rot<8, true>(a, f); break;
-        case 16: dispatch_rot<16, true>(a, f); break;
-        default: dispatch_rot<32, true>(a, f); break;
+        case 2: vec ? dispatch_rot<2, true>(a, f) : dispatch_rot<2, false>(a, f); break;
+        case 4: vec ? dispatch_rot<4, true>(a, f) : dispatch_rot<4, false>(a, f); break;
+        case 8: vec ? dispatch_rot<8, true>(a, f) : dispatch_rot<8, false>(a, f); break;
+        case 16: vec ? dispatch_rot<16, true>(a, f) : dispatch_rot<16, false>(a, f); break;
+        default: vec ? dispatch_rot<32, true>(a, f) : dispatch_rot<32, false>(a, f); break;
     }
 }
 
@@ -528,10 +536,9 @@ static gdr_status norm_fill(NormArgs& a, const long long* strides, int nstrides,
 }
 
 // The 16-byte form: rows of whole 8-element vectors, every stride a multiple
-// of 8, every pointer 16-byte aligned, and half-layout partners in whole vectors.
+// of 8, every pointer 16-byte aligned.
 static bool norm_vector(const NormArgs& a, bool bwd, size_t eg) {
     if (a.d % 8) return false;
-    if (a.rot && !a.interleaved && a.rot % 16) return false;
     for (const void* p : {a.q, a.k, a.qw, a.kw, (const void*)a.q_out, (const void*)a.k_out, a.gq, a.gk})
         if (!aligned_to(p, 16)) return false;
     for (int i = 0; i < 3; ++i)
@@ -561,7 +568,7 @@ gdr_status gdr_qk_norm_fwd(const void* q, const void* k, const void* q_weight, c
     if (!aligned_to(q_out, e) || !aligned_to(k_out, e)) return GDR_ERR_MISALIGNED;
     a.q_out = q_out; a.k_out = k_out;
     const bool vec = norm_vector(a, false, e);
-    const int lanes = vec ? norm_lanes(d) : 32;
+    const int lanes = norm_lanes(d);
     a.tpb = norm_tokens_per_block(a.tokens, lanes, H_q + H_k, 148 * kFwdBlocks);
     const long long grid = (a.tokens + a.tpb - 1) / a.tpb;
     if (grid > 0x7fffffffll) return GDR_ERR_UNSUPPORTED;
@@ -615,7 +622,7 @@ gdr_status gdr_qk_norm_bwd(const void* q, const void* k, const void* q_weight, c
     long long grid = 0;
     if (T > 0) {
         const bool vec = norm_vector(a, true, eg);
-        const int lanes = vec ? norm_lanes(d) : 32;
+        const int lanes = norm_lanes(d);
         a.tpb = norm_tokens_per_block(a.tokens, lanes, H_q + H_k, kNormMaxParts);
         grid = (a.tokens + a.tpb - 1) / a.tpb;
         if (grid > kNormMaxParts) grid = kNormMaxParts;

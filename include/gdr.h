@@ -523,8 +523,8 @@ gdr_status gdr_scan_step(const void* u, const void* delta, const float* A, const
  * dense (likewise k). 1 <= d <= 256, rot even and at most d, eps > 0. Angles
  * are reduced exactly, with inv_freq / (2 pi) held to 53 bits: an error of
  * position * inv_freq * 2^-53 radians. A row's sum of squares must stay within
- * fp32. Loads and stores are wide where d is a multiple of 8, strides likewise,
- * arrays are 16-byte aligned and, in the half layout, rot is a multiple of 16.
+ * fp32. Loads and stores are wide where d is a multiple of 8, strides likewise
+ * and arrays are 16-byte aligned.
  */
 gdr_status gdr_qk_norm_fwd(const void* q, const void* k, const void* q_weight,
                            const void* k_weight, const void* positions, const float* inv_freq,

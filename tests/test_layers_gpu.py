@@ -278,6 +278,11 @@ NORM = [  # dtype, weight type, grad type, B, T, Hq, Hk, d, rot, layout, kind, p
     (BF, BF, BF, 1, 700, 2, 2, 16, 16, "half", "rms", None, 1.0),
     (BF, None, F32, 1, 7, 3, 0, 200, 0, "half", "l2", None, 2.0),
     (F32, None, F32, 1, 3, 40, 40, 255, 254, "half", "rms", None, 1.0),
+    (BF, BF, BF, 2, 21, 3, 2, 104, 104, "half", "rms", torch.int64, 1.0),
+    (BF, None, F32, 3, 9, 5, 1, 24, 12, "half", "l2", torch.int32, 1.0),
+    (F32, F32, F32, 2, 13, 2, 2, 256, 250, "half", "rms", None, 0.5),
+    (BF, BF, BF, 2, 11, 2, 1, 114, 56, "half", "rms", torch.int64, 1.0),
+    (BF, None, BF, 1, 50, 3, 3, 30, 30, "interleaved", "l2", None, 1.0),
 ]
 
 
