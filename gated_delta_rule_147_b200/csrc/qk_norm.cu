@@ -46,7 +46,7 @@ struct NormArgs {
     float* part;                    // backward: weight-gradient partials [blocks][2][d], or null
     long long qs[3], ks[3], gqs[3], gks[3], ps[2];
     long long tokens;
-    int T, Hq, Hk, d, rot, tpb, rms, interleaved, pos64, w_f32;
+    int T, Hq, Hk, d, rot, tpb, rms, interleaved, pos64, w_f32, pairs;
     float eps, q_scale, rscale, inv_d, inv_eps;
 };
 
@@ -86,21 +86,30 @@ __device__ __forceinline__ void fill_turns(const NormArgs& a, long long tok0, fl
     }
 }
 
-// One lane's 8 elements of a row: e(i) = 8 li + i (VEC), or li + L i.
-template <int L, bool VEC> __device__ __forceinline__ int row_elem(int li, int i) { return VEC ? 8 * li + i : li + L * i; }
+// One lane's 8 elements of a row: 8 li + i (VEC), or the pairs li + L j.
+template <int L, bool VEC> __device__ __forceinline__ int row_elem(int li, int i) { return VEC ? 8 * li + i : 2 * (li + L * (i >> 1)) + (i & 1); }
 
 // The elements as loaded, and as numbers. A lane's elements from d on are
 // never loaded and stay 0; a row that is not wanted keeps what it held.
 template <typename T, int L, bool VEC> struct LaneRow {
     RawVec<T, 8> v;
-    __device__ __forceinline__ void load(const T* row, int li, int d, bool on) {
+    __device__ __forceinline__ void load(const T* row, int li, int d, bool on, int pairs) {
         if constexpr (VEC) {
             if (on) v.load(row);
+        } else if (pairs) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                RawVec<T, 2> p;
+                if (!on || row_elem<L, VEC>(li, 2 * j) >= d) continue;
+                p.load(row + 2 * L * j);
+#pragma unroll
+                for (int i = 0; i < RawVec<T, 2>::kWords; ++i) v.w[RawVec<T, 2>::kWords * j + i] = p.w[i];
+            }
         } else {
             if (on) v.zero();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (on && li + L * i < d) v.set(i, row[L * i]);
+                if (on && row_elem<L, VEC>(li, i) < d) v.set(i, row[row_elem<L, VEC>(0, i)]);
         }
     }
     __device__ __forceinline__ void get(f2 (&f)[4]) const {
@@ -109,16 +118,20 @@ template <typename T, int L, bool VEC> struct LaneRow {
     }
 };
 template <typename T, int L, bool VEC>
-__device__ __forceinline__ void store_lane(T* row, const f2 (&v)[4], int li, int d) {
+__device__ __forceinline__ void store_lane(T* row, const f2 (&v)[4], int li, int d, int pairs) {
     float f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
     if constexpr (VEC) {
         VecIO<T, 8>::store(row, f);
+    } else if (pairs) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (row_elem<L, VEC>(li, 2 * j) < d) VecIO<T, 2>::store(row + 2 * L * j, f + 2 * j);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (li + L * i < d) row[L * i] = from_f32<T>(f[i]);
+            if (row_elem<L, VEC>(li, i) < d) row[row_elem<L, VEC>(0, i)] = from_f32<T>(f[i]);
     }
 }
 
@@ -137,7 +150,7 @@ template <int L, bool VEC> __device__ __forceinline__ void lane_weight(f2 (&w)[4
         VecIO<float, 8>::load(f, sw + 8 * li);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = sw[li + L * i];
+        for (int i = 0; i < 8; ++i) f[i] = sw[row_elem<L, VEC>(li, i)];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = pack2(f[2 * i], f[2 * i + 1]);
@@ -177,14 +190,14 @@ __device__ __forceinline__ void lane_turns(f2 (&c)[4], f2 (&s)[4], const NormArg
 
 // Turns a lane's elements in place. src: the lane of the half layout's
 // partners (its own where not rotated). buf: the lane group's row in shared
-// memory (kHalfShared and the plain form).
+// memory (kHalfShared, and kHalf of the plain form).
 template <int L, bool VEC, int ROT>
 __device__ __forceinline__ void rotate(f2 (&y)[4], const f2 (&c)[4], const f2 (&s)[4], const NormArgs& a, int li,
                                        int src, float* buf) {
     float f[8], o[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) unpack2(y[i], f[2 * i], f[2 * i + 1]);
-    if constexpr (VEC && ROT == kInterleaved) {
+    if constexpr (ROT == kInterleaved) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = f[i ^ 1];
     } else if constexpr (VEC && ROT == kHalf) {
@@ -197,13 +210,13 @@ __device__ __forceinline__ void rotate(f2 (&y)[4], const f2 (&c)[4], const f2 (&
             VecIO<float, 8>::store(buf + 8 * li, f);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) buf[li + L * i] = f[i];
+            for (int i = 0; i < 8; ++i) buf[row_elem<L, VEC>(li, i)] = f[i];
         }
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int e = row_elem<L, VEC>(li, i);
-            o[i] = e < a.rot ? buf[ROT == kInterleaved ? e ^ 1 : (e < half ? e + half : e - half)] : 0.f;
+            o[i] = e < a.rot ? buf[e < half ? e + half : e - half] : 0.f;
         }
     }
 #pragma unroll
@@ -253,7 +266,7 @@ __device__ __forceinline__ HeadRows<T> output_rows(void* q, void* k, long long t
 template <typename T, int L, bool VEC, int ROT>
 __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(NormArgs a) {
     extern __shared__ float sm[];
-    constexpr bool kBuf = !VEC || ROT == kHalfShared;
+    constexpr bool kBuf = (!VEC && ROT == kHalf) || ROT == kHalfShared;
     __shared__ __align__(16) float rowbuf[kBuf ? kNormThreads / L : 1][kBuf ? 8 * L : 1];
     __shared__ __align__(16) float sw[512];
     constexpr int kSlots = kNormThreads / L, kAhead = sizeof(T) == 2 ? kFwdAhead : kFwdAhead / 2;
@@ -274,7 +287,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(N
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
         row[j].v.zero();
-        row[j].load(in.at(h0 + j * spt), li, a.d, h0 + j * spt < last);
+        row[j].load(in.at(h0 + j * spt), li, a.d, h0 + j * spt < last, a.pairs);
     }
     if (weighted) fill_weights<T>(sw, a, a.q_scale);
     if (ROT) fill_turns(a, tok0, cs, sn);
@@ -289,7 +302,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(N
             const int h = hb + h0 + j * spt, ahead = h + kAhead * spt;
             f2 y[4];
             row[j].get(y);
-            row[j].load(in.at(ahead), li, a.d, ahead < last);
+            row[j].load(in.at(ahead), li, a.d, ahead < last, a.pairs);
             f2 sq = mul2(y[0], y[0]);
 #pragma unroll
             for (int i = 1; i < 4; ++i) sq = fma2(y[i], y[i], sq);
@@ -306,7 +319,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(N
                 for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], both2(r));
             }
             if constexpr (ROT != 0) rotate<L, VEC, ROT>(y, c, s, a, li, src, buf);
-            if (h < last) store_lane<T, L, VEC>(out.at(h), y, li, a.d);
+            if (h < last) store_lane<T, L, VEC>(out.at(h), y, li, a.d, a.pairs);
         }
     }
 }
@@ -314,7 +327,7 @@ __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(N
 template <typename T, typename TG, int L, bool VEC, int ROT>
 __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(NormArgs a) {
     extern __shared__ float sm[];
-    constexpr bool kBuf = !VEC || ROT == kHalfShared;
+    constexpr bool kBuf = (!VEC && ROT == kHalf) || ROT == kHalfShared;
     __shared__ __align__(16) float rowbuf[kBuf ? kNormThreads / L : 1][kBuf ? 8 * L : 1];
     __shared__ __align__(16) float sw[512];
     constexpr int kSlots = kNormThreads / L, kAhead = sizeof(T) == 2 ? kBwdAhead : 1;
@@ -347,8 +360,8 @@ __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(N
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int h = h0 + j * spt;
-            xrow[j].load(in.at(h), li, a.d, h < last);
-            grow[j].load(gin.at(h), li, a.d, h < last);
+            xrow[j].load(in.at(h), li, a.d, h < last, a.pairs);
+            grow[j].load(gin.at(h), li, a.d, h < last, a.pairs);
         }
         f2 c[4], s[4];  // of the transposed rotation
         __syncthreads();  // the last tokens' turns have been read
@@ -365,8 +378,8 @@ __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(N
                 f2 x[4], g[4], gw[4];
                 xrow[j].get(x);
                 grow[j].get(g);
-                xrow[j].load(in.at(ahead), li, a.d, ahead < last);
-                grow[j].load(gin.at(ahead), li, a.d, ahead < last);
+                xrow[j].load(in.at(ahead), li, a.d, ahead < last, a.pairs);
+                grow[j].load(gin.at(ahead), li, a.d, ahead < last, a.pairs);
                 if constexpr (ROT != 0) rotate<L, VEC, ROT>(g, c, s, a, li, src, buf);
                 if (weighted) {
                     lane_weight<L, VEC>(gw, sw + (isq ? 0 : 256), li);
@@ -401,7 +414,7 @@ __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(N
 #pragma unroll
                         for (int i = 0; i < 4; ++i) dkw[i] = fma2(g[i], x[i], dkw[i]);
                     }
-                    store_lane<float, L, VEC>(out.at(h), dx, li, a.d);
+                    store_lane<float, L, VEC>(out.at(h), dx, li, a.d, a.pairs);
                 }
             }
         }
@@ -535,15 +548,16 @@ static gdr_status norm_fill(NormArgs& a, const long long* strides, int nstrides,
     return GDR_OK;
 }
 
-// The 16-byte form: rows of whole 8-element vectors, every stride a multiple
-// of 8, every pointer 16-byte aligned.
-static bool norm_vector(const NormArgs& a, bool bwd, size_t eg) {
-    if (a.d % 8) return false;
-    for (const void* p : {a.q, a.k, a.qw, a.kw, (const void*)a.q_out, (const void*)a.k_out, a.gq, a.gk})
-        if (!aligned_to(p, 16)) return false;
+// Rows of whole vectors of m elements: every stride a multiple of m, every
+// pointer (types of e, eg and eo bytes: inputs, gradients, outputs) aligned to
+// m elements, or 16 bytes.
+static bool norm_rows_aligned(const NormArgs& a, int m, bool bwd, size_t e, size_t eg, size_t eo) {
+    auto to = [&](size_t size) { return m * size < 16 ? m * size : 16; };
+    if (a.d % m || !aligned_to(a.q, to(e)) || !aligned_to(a.k, to(e)) || !aligned_to(a.gq, to(eg)) ||
+        !aligned_to(a.gk, to(eg)) || !aligned_to(a.q_out, to(eo)) || !aligned_to(a.k_out, to(eo)))
+        return false;
     for (int i = 0; i < 3; ++i)
-        if (a.qs[i] % 8 || a.ks[i] % 8 || (bwd && (a.gqs[i] % 8 || a.gks[i] % 8))) return false;
-    (void)eg;
+        if (a.qs[i] % m || a.ks[i] % m || (bwd && (a.gqs[i] % m || a.gks[i] % m))) return false;
     return true;
 }
 
@@ -567,7 +581,8 @@ gdr_status gdr_qk_norm_fwd(const void* q, const void* k, const void* q_weight, c
     const size_t e = dtype_size(dtype);
     if (!aligned_to(q_out, e) || !aligned_to(k_out, e)) return GDR_ERR_MISALIGNED;
     a.q_out = q_out; a.k_out = k_out;
-    const bool vec = norm_vector(a, false, e);
+    const bool vec = norm_rows_aligned(a, 8, false, e, e, e);
+    a.pairs = norm_rows_aligned(a, 2, false, e, e, e);
     const int lanes = norm_lanes(d);
     a.tpb = norm_tokens_per_block(a.tokens, lanes, H_q + H_k, 148 * kFwdBlocks);
     const long long grid = (a.tokens + a.tpb - 1) / a.tpb;
@@ -621,7 +636,9 @@ gdr_status gdr_qk_norm_bwd(const void* q, const void* k, const void* q_weight, c
     a.part = weights ? reinterpret_cast<float*>(workspace) : nullptr;
     long long grid = 0;
     if (T > 0) {
-        const bool vec = norm_vector(a, true, eg);
+        const size_t e = dtype_size(dtype);
+        const bool vec = norm_rows_aligned(a, 8, true, e, eg, 4);
+        a.pairs = norm_rows_aligned(a, 2, true, e, eg, 4);
         const int lanes = norm_lanes(d);
         a.tpb = norm_tokens_per_block(a.tokens, lanes, H_q + H_k, kNormMaxParts);
         grid = (a.tokens + a.tpb - 1) / a.tpb;
