@@ -60,25 +60,39 @@ __device__ __forceinline__ void token_of(const NormArgs& a, long long tok, long 
     t = tok - b * a.T;
 }
 
+// What the turns of a block's tokens are made of: each pair's turns per position
+// as a binary fraction, and the tokens' positions.
+struct TurnParts {
+    unsigned long long frac[128];
+    long long pos[16];
+};
+__device__ __forceinline__ void fill_frequencies(TurnParts& tp, const NormArgs& a) {
+    for (int p = threadIdx.x; p < a.rot / 2; p += kNormThreads) {
+        double f = (double)a.inv_freq[p] * 0.15915494309189535;  // 1 / (2 pi)
+        f -= floor(f);
+        tp.frac[p] = (unsigned long long)(f * 18446744073709551616.0);
+    }
+}
+__device__ __forceinline__ void fill_positions(TurnParts& tp, const NormArgs& a, long long tok0) {
+    const int i = kNormThreads - 1 - threadIdx.x;  // threads that the frequencies leave free
+    const long long tok = tok0 + i;
+    if (i >= a.tpb || tok >= a.tokens) return;
+    long long b, t;
+    token_of(a, tok, b, t);
+    if (a.pos) {
+        const long long o = b * a.ps[0] + t * a.ps[1];
+        t = a.pos64 ? reinterpret_cast<const long long*>(a.pos)[o] : reinterpret_cast<const int*>(a.pos)[o];
+    }
+    tp.pos[i] = t;
+}
 // cos and sin (times rscale) of the pairs of `tpb` tokens from token tok0.
-__device__ __forceinline__ void fill_turns(const NormArgs& a, long long tok0, float* cs, float* sn) {
-    const int half = a.rot / 2;
-    for (int i = threadIdx.x; i < a.tpb * half; i += kNormThreads) {
-        const int tk = i / half, p = i - tk * half;
-        const long long tok = tok0 + tk;
+__device__ __forceinline__ void fill_turns(const TurnParts& tp, const NormArgs& a, long long tok0, float* cs, float* sn) {
+    const unsigned half = a.rot / 2;
+    for (unsigned i = threadIdx.x; i < a.tpb * half; i += kNormThreads) {
+        const unsigned tk = i / half, p = i - tk * half;
         float c = 1.f, s = 0.f;
-        if (tok < a.tokens) {
-            long long b, t;
-            token_of(a, tok, b, t);
-            long long pos = t;
-            if (a.pos) {
-                const long long o = b * a.ps[0] + t * a.ps[1];
-                pos = a.pos64 ? reinterpret_cast<const long long*>(a.pos)[o] : reinterpret_cast<const int*>(a.pos)[o];
-            }
-            double f = (double)a.inv_freq[p] * 0.15915494309189535;  // turns per position
-            f -= floor(f);
-            const unsigned long long frac = (unsigned long long)(f * 18446744073709551616.0);
-            const long long turn = (long long)((unsigned long long)pos * frac);
+        if (tok0 + tk < a.tokens) {
+            const long long turn = (long long)((unsigned long long)tp.pos[tk] * tp.frac[p]);
             sincospif((float)turn * 0x1p-63f, &s, &c);
         }
         cs[i] = c * a.rscale;
@@ -290,7 +304,13 @@ __global__ void __launch_bounds__(kNormThreads, kFwdBlocks) qk_norm_fwd_kernel(N
         row[j].load(in.at(h0 + j * spt), li, a.d, h0 + j * spt < last, a.pairs);
     }
     if (weighted) fill_weights<T>(sw, a, a.q_scale);
-    if (ROT) fill_turns(a, tok0, cs, sn);
+    if constexpr (ROT != 0) {
+        __shared__ TurnParts tp;
+        fill_frequencies(tp, a);
+        fill_positions(tp, a, tok0);
+        __syncthreads();
+        fill_turns(tp, a, tok0, cs, sn);
+    }
     if (weighted || ROT) __syncthreads();
     f2 c[4], s[4];
     if (ROT) lane_turns<L, VEC, ROT>(c, s, a, cs + (slot / spt) * (a.rot / 2), sn + (slot / spt) * (a.rot / 2), li, 1.f);
@@ -340,6 +360,8 @@ __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(N
 #pragma unroll
     for (int i = 0; i < 4; ++i) dqw[i] = dkw[i] = both2(0.f);
     if (weighted) fill_weights<T>(sw, a, 1.f);
+    __shared__ TurnParts tp;
+    if (ROT) fill_frequencies(tp, a);
     float* buf = rowbuf[kBuf ? slot : 0];
     LaneRow<T, L, VEC> xrow[kAhead];
     LaneRow<TG, L, VEC> grow[kAhead];
@@ -364,9 +386,10 @@ __global__ void __launch_bounds__(kNormThreads, kBwdBlocks) qk_norm_bwd_kernel(N
             grow[j].load(gin.at(h), li, a.d, h < last, a.pairs);
         }
         f2 c[4], s[4];  // of the transposed rotation
+        if (ROT) fill_positions(tp, a, tok0);
         __syncthreads();  // the last tokens' turns have been read
         if (ROT) {
-            fill_turns(a, tok0, cs, sn);
+            fill_turns(tp, a, tok0, cs, sn);
             __syncthreads();
             lane_turns<L, VEC, ROT>(c, s, a, cs + (slot / spt) * (a.rot / 2), sn + (slot / spt) * (a.rot / 2), li, -1.f);
         }
