@@ -32,15 +32,15 @@ struct ConvShape {
 };
 
 // Filter taps and bias of V channels (`left` of them real).
-template <typename T, int V, int W, bool VEC>
+template <typename T, int V, int W, int HOW>
 __device__ __forceinline__ void load_taps(f2 (&w)[W][V / 2], f2 (&bias)[V / 2], const void* weight, const void* bp,
                                           int c, int left, int w_f32) {
     float flat[V * W], bf[V];  // [V][W], as the rows of [D, W] lie
-    if (VEC && w_f32) {
+    if (HOW == kWholeRow && w_f32) {
 #pragma unroll
         for (int i = 0; i < V * W; i += 4)
             VecIO<float, 4>::load(flat + i, reinterpret_cast<const float*>(weight) + (size_t)c * W + i);
-    } else if (VEC) {
+    } else if (HOW == kWholeRow) {
 #pragma unroll
         for (int i = 0; i < V * W; i += V)
             VecIO<T, V>::load(flat + i, reinterpret_cast<const T*>(weight) + (size_t)c * W + i);
@@ -66,13 +66,13 @@ __device__ __forceinline__ void load_taps(f2 (&w)[W][V / 2], f2 (&bias)[V / 2], 
 
 // The W - 1 inputs before row t0 of a sequence of n tokens (negative rows come
 // from X0); rows from n on are not read.
-template <typename T, int V, int W, bool VEC>
+template <typename T, int V, int W, int HOW>
 __device__ __forceinline__ void load_window(f2 (&win)[W][V / 2], const T* xr, const T* X0r, long long xt, int D, int t0,
                                             int n, int left) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         const int r = t0 - (W - 1) + j;
-        RowIO<T, V, VEC> row;
+        RowIO<T, V, HOW> row;
         row.zero();
         if (r >= 0 && r < n) row.load(xr + r * xt, left);
         else if (r < 0 && X0r) row.load(X0r + (size_t)(r + W - 1) * D, left);
@@ -88,13 +88,13 @@ template <int P, int W> __device__ __forceinline__ void slide(f2 (&win)[W][P]) {
         for (int i = 0; i < P; ++i) win[j][i] = win[j + 1][i];
 }
 
-template <typename T, int V, int W, bool VEC>
+template <typename T, int V, int W, int HOW>
 __global__ void __launch_bounds__(128) conv_fwd_kernel(const T* __restrict__ x, const void* __restrict__ weight,
                                                        const void* __restrict__ bias, const T* X0,
                                                        const int* __restrict__ lengths, T* __restrict__ y, T* X_T,
                                                        long long xb, long long xt, ConvShape s) {
     constexpr int P = V / 2, K = kConvAhead;
-    using Row = RowIO<T, V, VEC>;
+    using Row = RowIO<T, V, HOW>;
     const unsigned idx = blockIdx.x * 128u + threadIdx.x;
     if (idx >= s.total) return;
     const unsigned r0 = idx / s.nvec;
@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const T* __restrict__ x, 
     T* yr = y + ((size_t)b * s.T + t0) * s.D + c;
 
     f2 w[W][P], bs[P], win[W][P];  // win[j]: row t - W + 1 + j
-    load_taps<T, V, W, VEC>(w, bs, weight, bias, c, left, s.w_f32);
-    load_window<T, V, W, VEC>(win, xr, X0r, xt, s.D, t0, n, left);
+    load_taps<T, V, W, HOW>(w, bs, weight, bias, c, left, s.w_f32);
+    load_window<T, V, W, HOW>(win, xr, X0r, xt, s.D, t0, n, left);
     // The first chunk writes the carried rows. X_T may be X0 itself: only this
     // thread reads these channels of X0, and win holds them all by now.
     if (chunk == 0 && X_T) {
@@ -183,16 +183,16 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const T* __restrict__ x, 
 // One chunk of tokens: dx of its rows (and dX0 in the first chunk), and the
 // chunk's partial dw, dbias. dx_s needs dp up to W - 1 tokens on, so the walk
 // runs W - 1 tokens past the chunk; those tokens' dw belongs to the next chunk.
-template <typename T, typename TG, int V, int W, bool VEC>
+template <typename T, typename TG, int V, int W, int HOW>
 __global__ void __launch_bounds__(128) conv_bwd_kernel(
     const T* __restrict__ x, const void* __restrict__ weight, const void* __restrict__ bias,
     const T* __restrict__ X0, const int* __restrict__ lengths, const TG* __restrict__ dy,
     const float* __restrict__ dX_T, float* __restrict__ dx, float* __restrict__ dX0, float* __restrict__ part,
     long long xb, long long xt, long long gb, long long gt, ConvShape s) {
     constexpr int P = V / 2, K = kConvAhead;
-    using Row = RowIO<T, V, VEC>;
-    using Grad = RowIO<TG, V, VEC>;
-    using Out = RowIO<float, V, VEC>;
+    using Row = RowIO<T, V, HOW>;
+    using Grad = RowIO<TG, V, HOW>;
+    using Out = RowIO<float, V, HOW>;
     const unsigned idx = blockIdx.x * 128u + threadIdx.x;
     if (idx >= s.total) return;
     const unsigned r0 = idx / s.nvec;
@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(128) conv_bwd_kernel(
     const T* X0r = X0 ? X0 + (size_t)b * (W - 1) * s.D + c : nullptr;
 
     f2 w[W][P], bs[P], win[W][P], dw[W][P], db[P], acc[W][P];  // acc[j]: dx of row t - W + 1 + j so far
-    load_taps<T, V, W, VEC>(w, bs, weight, bias, c, left, s.w_f32);
-    load_window<T, V, W, VEC>(win, xr, X0r, xt, s.D, t0, n, left);
+    load_taps<T, V, W, HOW>(w, bs, weight, bias, c, left, s.w_f32);
+    load_window<T, V, W, HOW>(win, xr, X0r, xt, s.D, t0, n, left);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         db[i] = both2(0.f);
@@ -358,12 +358,12 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(const float* __restric
 
 // SEQ sequences of V channels per thread: with several, the taps are read once
 // for all of them and more rows are on their way.
-template <typename T, int V, int W, bool VEC, int SEQ>
+template <typename T, int V, int W, int HOW, int SEQ>
 __global__ void __launch_bounds__(128) conv_step_kernel(const T* __restrict__ x, const void* __restrict__ weight,
                                                         const void* __restrict__ bias, T* __restrict__ X,
                                                         T* __restrict__ y, long long xb, int B, ConvShape s) {
     constexpr int P = V / 2;
-    using Row = RowIO<T, V, VEC>;
+    using Row = RowIO<T, V, HOW>;
     dependent_launch();
     const unsigned idx = blockIdx.x * 128u + threadIdx.x;
     if (idx >= s.total) return;
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const T* __restrict__ x,
         for (int j = 0; j < W - 1; ++j) rows[q][j].load(Xr + (size_t)j * s.D, left);
         rows[q][W - 1].load(x + b * xb + c, left);
     }
-    load_taps<T, V, W, VEC>(w, bs, weight, bias, c, left, s.w_f32);
+    load_taps<T, V, W, HOW>(w, bs, weight, bias, c, left, s.w_f32);
 #pragma unroll
     for (int q = 0; q < SEQ; ++q) {
         const int b = b0 * SEQ + q;
@@ -448,16 +448,23 @@ static gdr_status conv_check(const void* weight, const void* bias, int B, int T,
     return GDR_OK;
 }
 
-// Wide loads: the channel count and every stride a multiple of the vector,
-// every pointer aligned to it.
-static bool conv_vector(int D, size_t e, const void* weight, std::initializer_list<const void*> ptrs,
-                        std::initializer_list<long long> strides) {
-    if (D % kConvVec || !aligned_to(weight, 16)) return false;
-    for (const void* p : ptrs)
-        if (!aligned_to(p, e * kConvVec)) return false;
-    for (long long st : strides)
-        if (st % kConvVec) return false;
-    return true;
+// How rows are accessed: vectors or pairs where the channel count and every
+// stride are multiples of theirs and every pointer is aligned to them.
+struct RowPtr { const void* p; size_t e; };
+static int conv_access(int D, const void* weight, std::initializer_list<RowPtr> ptrs,
+                       std::initializer_list<long long> strides) {
+    auto fits = [&](int m) {
+        bool ok = D % m == 0;
+        for (const RowPtr& r : ptrs) ok = ok && aligned_to(r.p, r.e * m);
+        for (long long st : strides) ok = ok && st % m == 0;
+        return ok;
+    };
+    return fits(kConvVec) && aligned_to(weight, 16) ? kWholeRow : fits(2) ? kPairRow : kSingleRow;
+}
+template <typename F> static void dispatch_access(int how, F&& f) {
+    if (how == kWholeRow) f(std::integral_constant<int, kWholeRow>());
+    else if (how == kPairRow) f(std::integral_constant<int, kPairRow>());
+    else f(std::integral_constant<int, kSingleRow>());
 }
 
 static cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -475,7 +482,7 @@ gdr_status gdr_conv_fwd(const void* x, const void* weight, const void* bias, con
         if (!aligned_to(p, e)) return GDR_ERR_MISALIGNED;
     if (!aligned_to(lengths, 4)) return GDR_ERR_MISALIGNED;
     const long long xb = strides ? strides[0] : (long long)T * D, xt = strides ? strides[1] : D;
-    const bool vec = conv_vector(D, e, weight, {x, X0, y, X_T}, {xb, xt});
+    const int how = conv_access(D, weight, {{x, e}, {X0, e}, {y, e}, {X_T, e}}, {xb, xt});
     ConvShape s = {};
     s.T = T; s.D = D; s.nvec = conv_vectors(D);
     s.tt = conv_fwd_tokens(B, T, s.nvec);
@@ -488,16 +495,15 @@ gdr_status gdr_conv_fwd(const void* x, const void* weight, const void* bias, con
     const unsigned grid = (unsigned)((total + 127) / 128);
     cudaStream_t st = as_stream(stream);
     dispatch_taps(W, [&](auto wc) {
-        constexpr int WT = decltype(wc)::value;
-#define GDR_CONV_FWD(TT, VEC)                                                                             \
-    conv_fwd_kernel<TT, kConvVec, WT, VEC><<<grid, 128, 0, st>>>((const TT*)x, weight, bias, (const TT*)X0, lengths, \
-                                                      (TT*)y, (TT*)X_T, xb, xt, s)
-        if (dtype == GDR_BF16) {
-            if (vec) GDR_CONV_FWD(__nv_bfloat16, true); else GDR_CONV_FWD(__nv_bfloat16, false);
-        } else {
-            if (vec) GDR_CONV_FWD(float, true); else GDR_CONV_FWD(float, false);
-        }
+        dispatch_access(how, [&](auto hc) {
+            constexpr int WT = decltype(wc)::value, HOW = decltype(hc)::value;
+#define GDR_CONV_FWD(TT)                                                                                             \
+    conv_fwd_kernel<TT, kConvVec, WT, HOW><<<grid, 128, 0, st>>>((const TT*)x, weight, bias, (const TT*)X0, lengths, \
+                                                                 (TT*)y, (TT*)X_T, xb, xt, s)
+            if (dtype == GDR_BF16) GDR_CONV_FWD(__nv_bfloat16);
+            else GDR_CONV_FWD(float);
 #undef GDR_CONV_FWD
+        });
     });
     return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
 }
@@ -527,9 +533,7 @@ gdr_status gdr_conv_bwd(const void* x, const void* weight, const void* bias, con
         if (!aligned_to(p, 4)) return GDR_ERR_MISALIGNED;
     const long long xb = strides ? strides[0] : (long long)T * D, xt = strides ? strides[1] : D;
     const long long gb = strides ? strides[2] : (long long)T * D, gt = strides ? strides[3] : D;
-    const bool vec = conv_vector(D, e, weight, {x, X0}, {xb, xt, gb, gt}) &&
-                     aligned_to(dy, eg * kConvVec) && aligned_to(dX_T, 4 * kConvVec) && aligned_to(dx, 4 * kConvVec) &&
-                     aligned_to(dX0, 4 * kConvVec);
+    const int how = conv_access(D, weight, {{x, e}, {X0, e}, {dy, eg}, {dX_T, 4}, {dx, 4}, {dX0, 4}}, {xb, xt, gb, gt});
     ConvShape s = {};
     s.T = T; s.D = D; s.nvec = conv_vectors(D);
     s.tt = conv_bwd_tokens(B, T, s.nvec);
@@ -543,18 +547,17 @@ gdr_status gdr_conv_bwd(const void* x, const void* weight, const void* bias, con
     cudaStream_t st = as_stream(stream);
     float* part = reinterpret_cast<float*>(workspace);
     dispatch_taps(W, [&](auto wc) {
-        constexpr int WT = decltype(wc)::value;
-#define GDR_CONV_BWD(TT, TG, VEC)                                                                              \
-    conv_bwd_kernel<TT, TG, kConvVec, WT, VEC><<<grid, 128, 0, st>>>((const TT*)x, weight, bias, (const TT*)X0, lengths, \
-                                                          (const TG*)dy, dX_T, dx, dX0, part, xb, xt, gb, gt, s)
-        if (dtype == GDR_FP32) { if (vec) GDR_CONV_BWD(float, float, true); else GDR_CONV_BWD(float, float, false); }
-        else if (grad_dtype == GDR_FP32) {
-            if (vec) GDR_CONV_BWD(__nv_bfloat16, float, true); else GDR_CONV_BWD(__nv_bfloat16, float, false);
-        } else {
-            if (vec) GDR_CONV_BWD(__nv_bfloat16, __nv_bfloat16, true);
-            else GDR_CONV_BWD(__nv_bfloat16, __nv_bfloat16, false);
-        }
+        dispatch_access(how, [&](auto hc) {
+            constexpr int WT = decltype(wc)::value, HOW = decltype(hc)::value;
+#define GDR_CONV_BWD(TT, TG)                                                                                         \
+    conv_bwd_kernel<TT, TG, kConvVec, WT, HOW><<<grid, 128, 0, st>>>((const TT*)x, weight, bias, (const TT*)X0,      \
+                                                                     lengths, (const TG*)dy, dX_T, dx, dX0, part, xb, \
+                                                                     xt, gb, gt, s)
+            if (dtype == GDR_FP32) GDR_CONV_BWD(float, float);
+            else if (grad_dtype == GDR_FP32) GDR_CONV_BWD(__nv_bfloat16, float);
+            else GDR_CONV_BWD(__nv_bfloat16, __nv_bfloat16);
 #undef GDR_CONV_BWD
+        });
     });
     if (cudaGetLastError() != cudaSuccess) return GDR_ERR_LAUNCH;
     const long long cols = (long long)(W + 1) * D;
@@ -571,7 +574,7 @@ gdr_status gdr_conv_step(const void* x, const void* weight, const void* bias, vo
     const size_t e = dtype_size(dtype);
     if (!aligned_to(x, e) || !aligned_to(X, e) || !aligned_to(y, e)) return GDR_ERR_MISALIGNED;
     const long long xb = strides ? strides[0] : D;
-    const bool vec = conv_vector(D, e, weight, {x, X, y}, {xb});
+    const int how = conv_access(D, weight, {{x, e}, {X, e}, {y, e}}, {xb});
     ConvShape s = {};
     s.T = 1; s.D = D; s.nvec = conv_vectors(D);
     s.silu = activation == GDR_ACT_SILU;
@@ -585,18 +588,18 @@ gdr_status gdr_conv_step(const void* x, const void* weight, const void* bias, vo
     cudaStream_t st = as_stream(stream);
     cudaError_t err = cudaErrorInvalidValue;
     dispatch_taps(W, [&](auto wc) {
-        constexpr int WT = decltype(wc)::value;
-#define GDR_CONV_STEP(TT, VEC)                                                                                     \
-    err = several ? launch_dependent(conv_step_kernel<TT, kConvVec, WT, VEC, 4>, grid, 128, 0, st, (const TT*)x, weight, \
-                                     bias, (TT*)X, (TT*)y, xb, B, s)                                               \
-                  : launch_dependent(conv_step_kernel<TT, kConvVec, WT, VEC, 1>, grid, 128, 0, st, (const TT*)x, weight, \
-                                     bias, (TT*)X, (TT*)y, xb, B, s)
-        if (dtype == GDR_BF16) {
-            if (vec) GDR_CONV_STEP(__nv_bfloat16, true); else GDR_CONV_STEP(__nv_bfloat16, false);
-        } else {
-            if (vec) GDR_CONV_STEP(float, true); else GDR_CONV_STEP(float, false);
-        }
+        dispatch_access(how, [&](auto hc) {
+            constexpr int WT = decltype(wc)::value, HOW = decltype(hc)::value;
+#define GDR_CONV_STEP(TT, SEQ)                                                                                       \
+    err = launch_dependent(conv_step_kernel<TT, kConvVec, WT, HOW, SEQ>, grid, 128, 0, st, (const TT*)x, weight, bias, \
+                           (TT*)X, (TT*)y, xb, B, s)
+            if (dtype == GDR_BF16) {
+                if (several) GDR_CONV_STEP(__nv_bfloat16, 4); else GDR_CONV_STEP(__nv_bfloat16, 1);
+            } else {
+                if (several) GDR_CONV_STEP(float, 4); else GDR_CONV_STEP(float, 1);
+            }
 #undef GDR_CONV_STEP
+        });
     });
     return err == cudaSuccess ? GDR_OK : GDR_ERR_LAUNCH;
 }

@@ -239,14 +239,27 @@ __device__ __forceinline__ float softplusf(float x) {
     return fmaf(r, y, fmaxf(x, 0.f));
 }
 
-// V channels (even) of one row, as loaded: wide loads (VEC), or one element at
-// a time where c + i < the row's length (`left` elements), others 0.
-template <typename T, int V, bool VEC> struct RowIO {
+// V channels (even) of one row, as loaded: a vector (kWholeRow), pairs, or one
+// element at a time where only that is aligned; of the last two `left` elements
+// exist, the others are 0.
+enum { kSingleRow = 0, kWholeRow = 1, kPairRow = 2 };
+template <typename T, int V, int HOW> struct RowIO {
     RawVec<T, V> v;
     __device__ __forceinline__ void zero() { v.zero(); }
     __device__ __forceinline__ void load(const T* p, int left) {
-        if constexpr (VEC) {
+        if constexpr (HOW == kWholeRow) {
             v.load(p);
+        } else if constexpr (HOW == kPairRow) {
+            constexpr int kWords = RawVec<T, 2>::kWords;
+            v.zero();
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                if (2 * i >= left) continue;
+                RawVec<T, 2> r;
+                r.load(p + 2 * i);
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) v.w[i * kWords + j] = r.w[j];
+            }
         } else {
             v.zero();
 #pragma unroll
@@ -259,8 +272,12 @@ template <typename T, int V, bool VEC> struct RowIO {
         float s[V];
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) unpack2(f[i], s[2 * i], s[2 * i + 1]);
-        if constexpr (VEC) {
+        if constexpr (HOW == kWholeRow) {
             VecIO<T, V>::store(p, s);
+        } else if constexpr (HOW == kPairRow) {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i)
+                if (2 * i < left) VecIO<T, 2>::store(p + 2 * i, s + 2 * i);
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)

@@ -67,6 +67,8 @@ CONV = [  # dtype, weight type, B, T, D, W, bias, state, lengths, silu, slice
     (BF, BF, 1, 3, 1, 4, True, True, False, True, 1),
     (BF, BF, 1, 0, 16, 4, True, True, False, True, 8),
     (BF, BF, 1, 4099, 8, 4, True, True, False, True, 8),
+    (BF, BF, 3, 41, 22, 4, True, True, True, True, 4),
+    (F32, F32, 2, 23, 18, 3, True, True, False, True, 2),
 ]
 
 
@@ -100,7 +102,7 @@ def test_conv(cuda_device, dtype, wdt, B, T, D, W, bias, state, ragg, act, pad):
     R.check(g2["dx"], v["dx"], m["dx"], 40, "dx without dX_T")
 
 
-@pytest.mark.parametrize("dtype,D,W", [(BF, 64, 4), (BF, 5, 3), (F32, 8, 2), (F32, 9, 4)])
+@pytest.mark.parametrize("dtype,D,W", [(BF, 64, 4), (BF, 5, 3), (F32, 8, 2), (F32, 9, 4), (BF, 30, 4)])
 def test_conv_steps_continue_the_sequence(cuda_device, dtype, D, W):
     """Prompt, then single tokens from the carried rows: bit for bit the whole
     sequence's outputs; the state may be carried in place."""
