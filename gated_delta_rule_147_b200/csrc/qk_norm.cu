@@ -31,9 +31,10 @@
 namespace gdr {
 
 // Rows a lane group requests ahead, and blocks per SM. Forward, 2 x 8192 tokens
-// of 64 heads of 128 in bf16: 4 and 3 take 95.5 us (5.6 TB/s), 2 and 3 106, 2 and
-// 4 103, 4 and 4 (spills) 103. Backward, 2 x 4096 tokens of 32 heads of 256: 3 and
-// 2 take 111 us (4.8 TB/s), 2 and 2 113, 1 and 2 135, 1 and 3 (spills) 131.
+// of 64 heads of 128 in bf16 (94 us, 5.7 TB/s): 4 and 3; 2 and 3 took 1.11 times
+// as long, 2 and 4 and 4 and 4 (spills) 1.08 times. Backward, 2 x 4096 tokens of
+// 32 heads of 256 (109 us, 4.9 TB/s): 3 and 2; 2 and 2 1.02 times, 1 and 2 and 1
+// and 3 (spills) about 1.2 times.
 constexpr int kFwdAhead = 4, kFwdBlocks = 3, kBwdAhead = 3, kBwdBlocks = 2;
 constexpr int kNormThreads = 256;
 constexpr int kNormMaxParts = 148 * kBwdBlocks;  // backward: one wave of blocks, each with sums of its own

@@ -18,7 +18,7 @@
 // conversions and global accesses fill the issue slots between its exponentials.
 // (All of it in one warp, with segments of 8 tokens per warp and their states
 // joined by a barrier per 64 tokens, ran at 0.47 instructions per cycle: 856 us
-// for 4 x 4096 tokens x 4096 channels x 16 states.)
+// for 4 x 4096 tokens x 4096 channels x 16 states, against 495 us.)
 #pragma once
 
 #include "layer_common.cuh"
@@ -72,12 +72,14 @@ template <int NS_, int CH_, int VW_, int STEPS_> struct ScanGeom {
     // the helpers move rows in vectors of VW channels
     static constexpr int VW = VW_ < CB ? VW_ : CB, VPT = CB / VW;
 };
-// Forward: 2 channels a lane and 2 blocks per SM take 478 us for 4 x 4096 tokens
-// x 4096 channels x 16 states, 1 channel and 4 blocks 579, 1 and 3 618. Backward
-// (its checkpoints too): 1 channel and 2 blocks 1130 us for 2 x 4096 x 4096 x 16
-// (ragged), 2 and 1 1325. Vectors: every helper thread has work with 16 states.
+// Forward, 4 x 4096 tokens x 4096 channels x 16 states (495 us): 2 channels a lane
+// and 2 blocks per SM; 1 channel and 4 blocks took 1.21 times as long, 1 and 3
+// 1.29 times. Backward, its checkpoints too, 2 x 4096 x 4096 x 16, ragged (1020
+// us): 1 channel and 2 blocks; 2 and 1 took 1.17 times as long. The vectors give
+// every helper thread work with 16 states.
 constexpr int kFwdBlocks = 2, kBwdBlocks = 2;
-// Steps of 16 tokens with 16 states (8: 531 us), of 32 where no sums are kept.
+// Steps of 16 tokens with 16 states (8 took 1.08 times as long), of 32 where no
+// sums are kept.
 template <int NS> using ScanFwdGeom = ScanGeom<NS, 2, 4, 1>;
 template <int NS> using ScanEndsGeom = ScanGeom<NS, 2, 4, 2>;
 template <int NS> using ScanBwdGeom = ScanGeom<NS, 1, 2, 1>;

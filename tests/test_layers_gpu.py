@@ -155,6 +155,9 @@ SCAN = [  # dtype, B, T, D, N, G, softplus, gate, skip, bias, state, lengths, sl
     (BF, 1, 1043, 40, 16, 1, True, True, True, True, True, False, 8),
     (F32, 3, 800, 9, 6, 1, True, True, True, True, True, True, 1),
     (BF, 2, 50, 300, 4, 1, True, True, True, True, True, False, 8),
+    (BF, 3, 43, 76, 6, 2, True, True, True, True, True, True, 2),
+    (BF, 1, 600, 22, 16, 1, True, True, True, True, True, False, 2),
+    (F32, 2, 45, 35, 10, 1, True, True, True, True, True, False, 1),
 ]
 
 
