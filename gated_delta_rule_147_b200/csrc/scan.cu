@@ -39,7 +39,7 @@ __device__ __forceinline__ void load_first(f2 (&s)[Gm::CH][2], const ScanArgs& a
     for (int c = 0; c < Gm::CH; ++c) lds_quad(s[c], p + (tl.part ? Gm::QUADS : 0) + c * 128);
 }
 
-template <typename T, typename Gm, int MODE>
+template <typename T, typename Gm, int MODE, bool WHOLE>
 __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * kFwdBlocks) scan_fwd_kernel(ScanArgs a) {
     constexpr int CH = Gm::CH, LT = Gm::LT, CB = Gm::CB, CL = Gm::CL, NP = Gm::NP;
     using Sh = ScanFwdShared<T, Gm, MODE == kScanOut>;
@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
         const int vch = Rows::channel(ht);
         T* y = reinterpret_cast<T*>(a.y) + (size_t)tl.b * a.T * a.D_ + tl.c0 + vch;
         using States = typename Sh::States;
+        const int rows = WHOLE ? (int)kWhole : a.act_vec, vecs = WHOLE ? (int)kWhole : a.bc_vec;
         Rows held_u[2], held_z[2];  // of the steps staged and walked
         uint32_t* const slots = reinterpret_cast<uint32_t*>(out + 2 * kOut);
         float bias[VW], skip[VW];
@@ -150,10 +151,10 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
             uint32_t* w = slots + (s & 1) * Sh::slots;
             if (s < steps) {
                 const int t0 = tl.t0 + s * LT;
-                if (copies_fit<T>(a.act_vec)) {
-                    Rows::fetch(w, dl, a.ds[1], t0, tl, a.act_vec, ht);
-                    Rows::fetch(w + Rows::kWords, u, a.us[1], t0, tl, a.act_vec, ht);
-                    if (z) Rows::fetch(w + 2 * Rows::kWords, z, a.zs[1], t0, tl, a.act_vec, ht);
+                if (copies_fit<T>(rows)) {
+                    Rows::fetch(w, dl, a.ds[1], t0, tl, rows, ht);
+                    Rows::fetch(w + Rows::kWords, u, a.us[1], t0, tl, rows, ht);
+                    if (z) Rows::fetch(w + 2 * Rows::kWords, z, a.zs[1], t0, tl, rows, ht);
                 } else {
                     Rows r[3];
                     r[0].load(dl, a.ds[1], t0, tl, ht);
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
                     r[1].store(w + Rows::kWords, ht);
                     if (z) r[2].store(w + 2 * Rows::kWords, ht);
                 }
-                States::fetch(w + 3 * Rows::kWords, Bm, Cm, a, t0, tl, ht);
+                States::fetch(w + 3 * Rows::kWords, Bm, Cm, a, t0, tl, vecs, ht);
             }
             copies_commit();
         };
@@ -252,7 +253,8 @@ template <typename T, int NS, int MODE> static cudaError_t launch_fwd_geom(const
     if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
     constexpr size_t smem = ScanFwdShared<T, Gm, MODE == kScanOut>::total * sizeof(float);
     static_assert(smem <= 227 * 1024, "shared memory of a block");
-    auto kern = scan_fwd_kernel<T, Gm, MODE>;
+    const bool whole = a.act_vec == kWhole && a.bc_vec == kWhole;
+    auto kern = whole ? scan_fwd_kernel<T, Gm, MODE, true> : scan_fwd_kernel<T, Gm, MODE, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)grid, kScanThreads, smem, st>>>(a);

@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                     if (z) r[2].store(w + 2 * Rows::kWords, ht);
                     g.store(w + kGrads, ht);
                 }
-                States::fetch(w + kStates, Bm, Cm, a, t0, tl, ht);
+                States::fetch(w + kStates, Bm, Cm, a, t0, tl, a.bc_vec, ht);
             }
             copies_commit();
         };

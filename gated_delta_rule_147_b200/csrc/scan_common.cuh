@@ -191,6 +191,8 @@ template <int LEFT> __device__ __forceinline__ void copies_wait() {
 // vec: kWhole vectors or kPairs of elements are aligned to their size, or only
 // elements are. Copies are of 4 bytes at least, so single bf16 elements take
 // plain loads (slot_load, then slot_store once all loads of a step are under way).
+// The forward kernels have an instance for whole vectors throughout: the other
+// forms' code cost it 3% (the backward one nothing).
 enum { kSingle = 0, kWhole = 1, kPairs = 2 };
 template <typename T> __device__ __forceinline__ bool copies_fit(int vec) { return sizeof(T) == 4 || vec != kSingle; }
 
@@ -304,14 +306,14 @@ template <typename T, typename Gm, int L> struct StateRows {
         return {p + (t0 + tok) * (e < kEach ? a.bs[1] : a.cs[1]) + n0, e < kAll && p, t0 + tok < tl.n && n0 < a.N, a.N - n0};
     }
     static __device__ __forceinline__ void fetch(uint32_t* slots, const T* Bp, const T* Cp, const ScanArgs& a, int t0,
-                                                 const ScanTile& tl, int ht) {
+                                                 const ScanTile& tl, int vec, int ht) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Source s = source(i, Bp, Cp, a, t0, tl, ht);
             uint32_t* slot = slots + (kHelperThreads * i + ht) * kVec;
-            if (s.any && copies_fit<T>(a.bc_vec)) slot_fetch<T, 4>(slot, s.p, s.on, s.left, a.bc_vec);
+            if (s.any && copies_fit<T>(vec)) slot_fetch<T, 4>(slot, s.p, s.on, s.left, vec);
         }
-        if (copies_fit<T>(a.bc_vec)) return;
+        if (copies_fit<T>(vec)) return;
         constexpr int kTogether = NV < 4 ? NV : 4;
 #pragma unroll
         for (int i0 = 0; i0 < NV; i0 += kTogether) {
