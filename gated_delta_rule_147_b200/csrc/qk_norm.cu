@@ -150,13 +150,17 @@ __device__ __forceinline__ void store_lane(T* row, const f2 (&v)[4], int li, int
     }
 }
 
-// q's and k's weights as fp32 in shared memory, rows of 256 (ones where absent).
+// q's and k's weights as fp32 in shared memory, rows of 256: ones where absent,
+// zeros from d on. Lanes read past d, and their elements there enter the row's
+// sums as 0 * weight, so what an earlier kernel left (NaN) must not stay.
 template <typename T> __device__ __forceinline__ void fill_weights(float* sw, const NormArgs& a, float q_scale) {
-    for (int i = threadIdx.x; i < 2 * a.d; i += kNormThreads) {
-        const int e = i < a.d ? i : i - a.d;
-        const void* p = i < a.d ? a.qw : a.kw;
-        const float w = !p ? 1.f : a.w_f32 ? reinterpret_cast<const float*>(p)[e] : to_f32(reinterpret_cast<const T*>(p)[e]);
-        sw[(i < a.d ? 0 : 256) + e] = i < a.d ? w * q_scale : w;
+    for (int i = threadIdx.x; i < 512; i += kNormThreads) {
+        const int e = i & 255;
+        const bool isq = i < 256;
+        const void* p = isq ? a.qw : a.kw;
+        float w = 0.f;
+        if (e < a.d) w = !p ? 1.f : a.w_f32 ? reinterpret_cast<const float*>(p)[e] : to_f32(reinterpret_cast<const T*>(p)[e]);
+        sw[i] = isq ? w * q_scale : w;
     }
 }
 template <int L, bool VEC> __device__ __forceinline__ void lane_weight(f2 (&w)[4], const float* sw, int li) {
@@ -496,7 +500,7 @@ static int norm_lanes(int d) {
 // groups then share a token's heads) make more blocks. Least cost of waves of
 // `blocks` blocks (backward: turns of that many), each the rows of a lane group
 // and about four rows' time for the cosines: 6 x 391 tokens of 6 heads of 67
-// backward take 45 us with one token a block, 9 with eight.
+// backward take 45 us with one token a block, 9 with the number taken here.
 static int norm_tokens_per_block(long long tokens, int lanes, int rows, long long blocks) {
     const int slots = kNormThreads / lanes;
     int best = 1;

@@ -319,6 +319,30 @@ def test_norm(cuda_device, dtype, wdt, gdt, B, T, Hq, Hk, d, rot, layout, kind, 
         assert torch.equal(qc, yq) and torch.equal(kc, yk)
 
 
+@pytest.mark.parametrize("d,pad", [(72, 0), (66, 0), (67, 1), (120, 0)])
+@pytest.mark.parametrize("layout,rot", [("half", 0), ("half", 32), ("interleaved", 32)])
+def test_norm_of_rows_narrower_than_their_lanes(cuda_device, d, pad, layout, rot):
+    """What an earlier call left in shared memory (here NaN weights of wider rows
+    on as many lanes) does not reach a row."""
+    r = Rnd(cuda_device, d)
+    f = torch.exp(-torch.arange(rot // 2) / 3.0).to(cuda_device) if rot else None
+    kws = dict(kind="rms", eps=1e-5, inv_freq=f, rotary=layout)
+    wide, bad = r(1, 2048, 1, 128 + pad)[..., :128], torch.full((128,), NAN, device=cuda_device)
+    if d % 8:  # rows that are no whole vectors either
+        wide = sliced(wide, 1)
+    q, k, dq, dk = (r(2, 300, 2, d + pad)[..., :d] for _ in range(4))
+    qw, kw = r(d), r(d)
+    gdr.qk_norm_bwd(wide, q_weight=bad, dq=wide, **kws)
+    g = gdr.qk_norm_bwd(q, k, qw, kw, dq=dq, dk=dk, **kws)
+    gdr.qk_norm_fwd(wide, q_weight=bad, **kws)
+    yq, yk = gdr.qk_norm_fwd(q, k, qw, kw, **kws)
+    for x, w, y, do, n in ((q, qw, yq, dq, "q"), (k, kw, yk, dk, "k")):
+        v, m = R.norm(x, w, "rms", 1e-5, 1.0, None, f, layout, 1.0, do)
+        R.check(y, v["y"], m["y"], 40, n)
+        R.check(g["d" + n], v["dx"], m["dx"], 100, "d" + n)
+        R.check(g[f"d{n}_weight"], v["dw"], m["dw"], 100 + 2 * 300 * 2, f"d{n}_weight")
+
+
 @pytest.mark.parametrize("kind", ["l2", "rms"])
 def test_norm_zero_and_tiny_rows(cuda_device, kind):
     """Rows of zeros and rows below eps: finite values and gradients."""
