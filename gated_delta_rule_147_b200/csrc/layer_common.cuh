@@ -133,6 +133,13 @@ __device__ __forceinline__ float sigmoidf_fast(float x) {
     return rcp_approx(1.f + ex2_approx(-x * kLog2e));
 }
 
+// The smaller one; NaN where either is (fminf drops it).
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // ---- packed pairs of fp32 (one instruction for two multiply-adds) ----
 typedef unsigned long long f2;
 __device__ __forceinline__ f2 pack2(float a, float b) {
@@ -190,9 +197,11 @@ __device__ __forceinline__ f2 decay2(f2 dt, f2 a) { return ex2_pair(fma2(dt, a, 
 // on [0, 1] (Remez exchange on log1p(y) / y): 3.1e-8, with fp32 arithmetic below
 // 3 2^-24. An error in a step size goes into every later state, so y gets back
 // what the product x log2(e) and log2(e) itself lost in rounding, and most of the
-// exponential's mean error (0.8 2^-24 below over arguments from -8 to -1).
+// exponential's mean error (0.8 2^-24 below over arguments from -8 to -1). |x| is
+// held to 128, where y is 0 already: the product and its rest must stay finite, for
+// a step input of -inf or the type's lowest number masks its token.
 // `sig`: the derivative, 1 / (1 + y) or y / (1 + y).
-__device__ __forceinline__ f2 exp_neg2(f2 x) {  // e^-x, x >= 0
+__device__ __forceinline__ f2 exp_neg2(f2 x) {  // e^-x, 0 <= x <= 128
     const f2 t = mul2(x, both2(kLog2e));  // 2^-t, and 2^r with the rest r of the exponent
     f2 r = fma2(x, both2(-kLog2e), t);
     r = fma2(x, both2(-1.925963033500e-08f), add2(r, both2(5e-8f)));
@@ -205,7 +214,7 @@ struct StepCurve { f2 dt, sig; };
 template <bool SIG> __device__ __forceinline__ StepCurve softplus2(f2 x) {
     float a, b;
     unpack2(x, a, b);
-    const f2 y = exp_neg2(pack2(fabsf(a), fabsf(b)));
+    const f2 y = exp_neg2(pack2(min_nan(fabsf(a), 128.f), min_nan(fabsf(b), 128.f)));
     float ya, yb;
     unpack2(y, ya, yb);
     f2 r = both2(0.0052326940931379795f);

@@ -462,7 +462,9 @@ gdr_status gdr_conv_step(const void* x, const void* weight, const void* bias, vo
  * [G, N] dense; A [D_, N] (negative for a decay; not enforced), D, delta_bias
  * [D_] or NULL, z NULL for no gate; h0, h_T [B, D_, N] fp32 or NULL (h0 = 0 /
  * not written), h_T may be h0; y [B, T, D_]. strides: batch and token of u,
- * delta, Bm, Cm, z. 1 <= N <= 128, D_ a multiple of G.
+ * delta, Bm, Cm, z. 1 <= N <= 128, D_ a multiple of G. With delta_softplus a
+ * delta of -inf or the type's lowest number is a step of 0: the token keeps the
+ * state.
  * workspace: NULL, or gdr_scan_fwd_workspace_size() bytes, 256-byte aligned;
  * with it the tokens are split where there are few channels (a size of 0 says
  * that they are not; a smaller workspace is not used). Contents on entry

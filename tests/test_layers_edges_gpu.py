@@ -1,0 +1,84 @@
+"""The layer operators at the ends of their ranges: steps that mask a token,
+values that are not finite, the longest sums, the most rows."""
+import pytest
+import torch
+
+import gated_delta_rule_147_b200 as gdr
+import layers_ref as R
+from test_layers_gpu import Rnd, scan_inputs
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+NAN, INF = float("nan"), float("inf")
+SEQ = ("u", "delta", "Bm", "Cm", "z")
+ARGS = ("u", "delta", "A", "Bm", "Cm", "D", "z", "h0")
+
+
+def same(a, b):
+    return torch.equal(torch.nan_to_num(a), torch.nan_to_num(b)) and torch.equal(a.isnan(), b.isnan())
+
+
+# ---------------------------------------------------------------- selective scan
+
+@pytest.mark.parametrize("dtype,B,T,D,N,G", [(F32, 2, 37, 12, 16, 1), (BF, 2, 70, 24, 4, 2), (BF, 1, 1030, 8, 16, 1),
+                                             (F32, 1, 600, 5, 3, 1)])
+@pytest.mark.parametrize("low", ["-inf", "lowest"])
+def test_scan_steps_that_mask_a_token(cuda_device, dtype, B, T, D, N, G, low):
+    """A step input of -inf, or the type's lowest number, is a step of 0: the token
+    keeps the state and has no gradient through it. Bit for bit what an input of
+    -200 gives (e^-200 is 0 in fp32), which the 64-bit form checks; the same in
+    prompts (also split ones), gradients and single tokens."""
+    r = Rnd(cuda_device, T + N)
+    i = scan_inputs(r, dtype, B, T, D, N, G, True, True, True, True, True)
+    masked = torch.zeros(B, T, D, dtype=torch.bool, device=cuda_device)
+    masked[:, 3::5] = True
+    masked[0, T // 2:T // 2 + 20] = True
+    masked[:, 0, ::2] = True
+    dy, dh = r(B, T, D), r(B, D, N)
+    kw = dict(delta_bias=i["delta_bias"], delta_softplus=True)
+    got = []
+    for v in (-200.0, -INF if low == "-inf" else torch.finfo(dtype).min):
+        a = dict(i, delta=torch.where(masked, torch.tensor(v, dtype=dtype, device=cuda_device), i["delta"]))
+        args = tuple(a[k] for k in ARGS)
+        y, h_T = gdr.scan_fwd(*args, **kw)
+        g = gdr.scan_bwd(*args, dy=dy, dh_T=dh, **kw)
+        h = i["h0"].clone()
+        steps = [gdr.scan_step(*(None if a[k] is None else a[k][:, t] if k in SEQ else a[k] for k in ARGS[:7]), h, **kw)
+                 for t in range(min(T, 24))]
+        got.append(dict(g, y=y, h_T=h_T, h=h, steps=torch.stack(steps, 1), whole=gdr.scan_fwd(*args, workspace=None, **kw)[0]))
+        if v == -200.0:
+            ref = R.scan(*args, i["delta_bias"], True, None, dy, dh)
+            for k in ref[0]:
+                R.check(got[0][k], ref[0][k], ref[2][k], 1, k)
+    for k, v in got[0].items():
+        assert torch.equal(v, got[1][k]), k
+    assert (got[1]["ddelta"][masked] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_scan_steps_at_the_upper_end(cuda_device, dtype):
+    """Huge and infinite steps, and NaN: softplus is the identity there; a prompt of one
+    token and a single token agree, and a NaN stays with its channel."""
+    B, D, N = 1, 8, 4
+    r = Rnd(cuda_device, 9)
+    i = scan_inputs(r, dtype, B, 1, D, N, 1, True, False, True, False, True)
+    i["u"] = i["u"] * 1e-30
+    for v in (1e10, 3e38, INF, NAN):
+        delta = i["delta"].clone()
+        delta[..., ::2] = v
+        args = (i["u"], delta, i["A"], i["Bm"], i["Cm"], i["D"], None)
+        y, h = gdr.scan_fwd(*args, i["h0"], delta_softplus=True)
+        h1 = i["h0"].clone()
+        y1 = gdr.scan_step(*(t[:, 0] if k in SEQ and t is not None else t for k, t in zip(ARGS, args)), h1,
+                           delta_softplus=True)
+        assert torch.equal(h.isnan(), h1.isnan()) and torch.equal(y[:, 0].isnan(), y1.isnan())
+        assert torch.isfinite(h[:, 1::2]).all() and torch.isfinite(y[..., 1::2]).all()
+        if v != v:
+            assert h[:, ::2].isnan().all()
+        else:
+            dtu = v * i["u"].double()[:, 0, ::2, None] if v == INF else delta.double()[:, 0, ::2, None] * i["u"].double()[:, 0, ::2, None]
+            want = (dtu * i["Bm"].double()[:, 0]).float()  # the decay is 0
+            for got in (h, h1):
+                ok = (got[:, ::2] == want) | ((got[:, ::2] - want).abs() <= 4 * R.U32 * want.abs())
+                assert ok.all()
