@@ -123,17 +123,20 @@ std::pair<char*, char*> span(const Tensor& t) {
     char* p = static_cast<char*>(t.data_ptr());
     return {p, p + n * (int64_t)t.element_size()};
 }
-// A given result t shares no memory with the others; `same` may be t's own
-// memory, whole.
-void apart(const char* name, Opt t, std::initializer_list<Named> others, Opt same = nullptr) {
+// A given result t shares no memory with the others. It may be `same`, the one
+// input that the call may overwrite, where that is dense (t is): rows in another
+// order over the same memory would be overwritten before they are read.
+void apart(const char* name, Opt t, std::initializer_list<Named> others, Named same = {nullptr, nullptr}) {
     if (!t || !t->numel()) return;
     const auto a = span(*t);
-    for (const Named& o : others) {
-        if (!o.t || !o.t->numel()) continue;
+    auto refuse = [&](const Named& o, bool whole) {
+        if (!o.t || !o.t->numel()) return;
         const auto b = span(*o.t);
-        if (same && o.t == same && b == a) continue;
+        if (whole && b == a && o.t->is_contiguous()) return;
         if (a.first < b.second && b.first < a.second) bad_value(std::string(name) + " overlaps " + o.name);
-    }
+    };
+    for (const Named& o : others) refuse(o, false);
+    refuse(same, true);
 }
 
 void* ptr(Opt t) { return t ? t->data_ptr() : nullptr; }
@@ -293,7 +296,7 @@ PyObject* conv_fwd(PyObject* const* a) {
     dense("out", out, {B, T, D}, c.own, dev);
     dense("lengths", lengths, {B}, at::kInt, dev);
     apart("out", out, {{"x", &c.x}, {"weight", &c.weight}, {"bias", c.bias}, {"lengths", lengths}, {"X0", X0}, {"X_T", XT}});
-    apart("X_T", XT, {{"x", &c.x}, {"weight", &c.weight}, {"bias", c.bias}, {"lengths", lengths}, {"X0", X0}}, X0);
+    apart("X_T", XT, {{"x", &c.x}, {"weight", &c.weight}, {"bias", c.bias}, {"lengths", lengths}}, {"X0", X0});
     const bool final_state = truth(a[7]);
     Where at(dev, a[9]);
     Tensor y, last;
@@ -407,7 +410,7 @@ PyObject* scan_fwd(PyObject* const* a) {
     apart("out", out, {{"u", &s.u}, {"delta", &s.delta}, {"A", &s.A}, {"Bm", &s.Bm}, {"Cm", &s.Cm}, {"D", s.D}, {"z", s.z},
                        {"h0", s.h}, {"delta_bias", s.bias}, {"lengths", lengths}, {"h_T", hT}});
     apart("h_T", hT, {{"u", &s.u}, {"delta", &s.delta}, {"A", &s.A}, {"Bm", &s.Bm}, {"Cm", &s.Cm}, {"D", s.D}, {"z", s.z},
-                      {"h0", s.h}, {"delta_bias", s.bias}, {"lengths", lengths}}, s.h);
+                      {"delta_bias", s.bias}, {"lengths", lengths}}, {"h0", s.h});
     bool split = a[11] != Py_None;
     Opt given = nullptr;
     if (PyUnicode_Check(a[11])) choice(a[11], "workspace", {{"auto", 0}}, "'auto', None or a tensor");
@@ -537,10 +540,10 @@ PyObject* qk_norm_fwd(PyObject* const* a) {
     dense("q_out", qo, {n.B, n.T, n.Hq, n.d}, n.q.scalar_type(), dev);
     if (ko && !n.k) bad_value("k_out without k");
     dense("k_out", ko, {n.B, n.T, n.Hk, n.d}, n.q.scalar_type(), dev);
-    apart("q_out", qo, {{"q_weight", n.qw}, {"k_weight", n.kw}, {"positions", n.pos}, {"inv_freq", n.freq}, {"q", &n.q},
-                        {"k", n.k}, {"k_out", ko}}, &n.q);
-    apart("k_out", ko, {{"q_weight", n.qw}, {"k_weight", n.kw}, {"positions", n.pos}, {"inv_freq", n.freq}, {"q", &n.q},
-                        {"k", n.k}}, n.k);
+    apart("q_out", qo, {{"q_weight", n.qw}, {"k_weight", n.kw}, {"positions", n.pos}, {"inv_freq", n.freq}, {"k", n.k},
+                        {"k_out", ko}}, {"q", &n.q});
+    apart("k_out", ko, {{"q_weight", n.qw}, {"k_weight", n.kw}, {"positions", n.pos}, {"inv_freq", n.freq}, {"q", &n.q}},
+          {"k", n.k});
     Where at(dev, a[13]);
     Tensor yq, yk;
     if (!qo) yq = at.empty({n.B, n.T, n.Hq, n.d}, n.q.scalar_type());
@@ -597,7 +600,9 @@ PyObject* check_tensor(PyObject* const* a) {
 // name, tensor, other name, other tensor, may be the same
 PyObject* check_apart(PyObject* const* a) {
     const Opt t = tensor(a[1], "tensor"), o = tensor(a[3], "tensor");
-    apart(PyUnicode_AsUTF8(a[0]), t, {{PyUnicode_AsUTF8(a[2]), o}}, truth(a[4]) ? o : nullptr);
+    const Named other = {PyUnicode_AsUTF8(a[2]), o};
+    if (truth(a[4])) apart(PyUnicode_AsUTF8(a[0]), t, {}, other);
+    else apart(PyUnicode_AsUTF8(a[0]), t, {other});
     Py_RETURN_NONE;
 }
 PyObject* set_error(PyObject* const* a) {

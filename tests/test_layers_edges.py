@@ -1,0 +1,22 @@
+"""The layer operators' host side at the ends of what they take (no GPU needed)."""
+import pytest
+import torch
+
+from gated_delta_rule_147_b200 import _lib, layers  # noqa: F401
+from gated_delta_rule_147_b200 import _layers
+
+P = 1 << 20  # a fake, aligned device address that no check follows
+
+
+def test_a_result_in_place_has_its_inputs_layout():
+    """The same bytes in another order are not the same rows."""
+    buf = torch.zeros(2, 3, 4, 8)
+    apart = _layers.check_apart
+    apart("q_out", buf, "q", buf, True)
+    apart("q_out", buf.view(6, 1, 4, 8), "q", buf, True)
+    with pytest.raises(ValueError, match="q_out overlaps q"):
+        apart("q_out", buf.view(2, 4, 3, 8), "q", buf.transpose(1, 2), True)
+    with pytest.raises(ValueError, match="q_out overlaps q"):
+        apart("q_out", buf, "q", buf[:, :, :, :1].expand(2, 3, 4, 8), True)
+    one = torch.zeros(2, 1, 4, 8)  # an axis of one has no order
+    apart("q_out", one.view(2, 4, 1, 8), "q", one.transpose(1, 2), True)

@@ -82,3 +82,34 @@ def test_scan_steps_at_the_upper_end(cuda_device, dtype):
             for got in (h, h1):
                 ok = (got[:, ::2] == want) | ((got[:, ::2] - want).abs() <= 4 * R.U32 * want.abs())
                 assert ok.all()
+
+
+# ---------------------------------------------------------------- results in place
+
+def test_in_place_refusals(cuda_device):
+    """A result may be its own input, dense; no other input, the same tensor given
+    twice included, and no other order of the rows."""
+    r = Rnd(cuda_device, 41)
+    buf = r(2, 3, 4, 16)
+    q, k = buf.transpose(1, 2), r(2, 4, 3, 16)
+    before = buf.clone()
+    with pytest.raises(ValueError, match="q_out overlaps q"):
+        gdr.qk_norm_fwd(q, k, q_out=buf.view(2, 4, 3, 16))
+    with pytest.raises(ValueError, match="k_out overlaps k"):
+        gdr.qk_norm_fwd(k, q, k_out=buf.view(2, 4, 3, 16))
+    with pytest.raises(ValueError, match="q_out overlaps k"):
+        gdr.qk_norm_fwd(buf, buf, q_out=buf)
+    with pytest.raises(ValueError, match="k_out overlaps q"):
+        gdr.qk_norm_fwd(buf, buf, k_out=buf)
+    x = r(2, 3, 8)
+    kept = x.clone()
+    with pytest.raises(ValueError, match="X_T overlaps x"):
+        gdr.conv_fwd(x, r(8, 4), None, x, X_T=x)
+    s = r(1, 4, 4)
+    with pytest.raises(ValueError, match="h_T overlaps u"):
+        gdr.scan_fwd(s, s.clone(), -torch.ones(4, 4, device=cuda_device), r(1, 4, 1, 4), r(1, 4, 1, 4), None, None, s, h_T=s)
+    torch.cuda.synchronize()
+    assert torch.equal(buf, before) and torch.equal(x, kept)
+    want, _ = gdr.qk_norm_fwd(buf)
+    got, _ = gdr.qk_norm_fwd(buf, q_out=buf)
+    assert got is buf and torch.equal(buf, want)
