@@ -133,10 +133,15 @@ __device__ __forceinline__ float sigmoidf_fast(float x) {
     return rcp_approx(1.f + ex2_approx(-x * kLog2e));
 }
 
-// The smaller one; NaN where either is (fminf drops it).
+// The smaller and the larger one; NaN where either is (fminf and fmaxf drop it).
 __device__ __forceinline__ float min_nan(float a, float b) {
     float y;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
 
@@ -189,6 +194,11 @@ __device__ __forceinline__ f2 sigmoid2(f2 x) {  // sigmoidf_fast of each
 // thousands of times, and the state came out twice as far off as with correctly
 // rounded exponentials. So the argument gets the 0.32 2^-24 / ln 2 back, in the
 // multiply-add that forms it; an argument of 0 still gives 1.
+__device__ __forceinline__ float decay_rate(float A) {  // A log2(e)
+    // A = -inf (a state that holds one token) times dt = 0 of a padded token would be
+    // NaN; the lowest number gives the same decays
+    return max_nan(A * kLog2e, -3.402823466e38f);
+}
 __device__ __forceinline__ f2 decay2(f2 dt, f2 a) { return ex2_pair(fma2(dt, a, both2(2.75e-8f))); }
 
 // log(1 + e^x) = max(x, 0) + log1p(y), y = e^-|x| in (0, 1], with log1p(y) = y Q(y):

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
     if (warp < kWalkers) {
         const int nl = lane % Gm::NS, cl = lane / Gm::NS, p0 = lane_place<Gm>(warp, 0, cl);
         f2 A[CH][2], h[CH][2];
-        load_states<Gm>(A, a.A, tl, a.N, a.state_vec, p0, nl, kLog2e, true);
+        load_states<Gm, true>(A, a.A, tl, a.N, a.state_vec, p0, nl);
         if (MODE == kScanOut && a.chunks > 1) {
             load_first<Gm>(h, a, tl, warp, lane);
             fold_chunks<Gm>(h, a.ends, a, tl, warp, lane, 1, tl.part, 1);
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(256, kStepBlocks) scan_step_kernel(ScanArgs a,
             const float dtc = __shfl_sync(0xffffffffu, dt, ch), dtu = __shfl_sync(0xffffffffu, dt * uf, ch);
             f2 yv = both2(0.f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) A[k][i] = fmaxf(A[k][i] * kLog2e, -3.402823466e38f);  // as load_states
+            for (int i = 0; i < 4; ++i) A[k][i] = decay_rate(A[k][i]);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 f2 v = fma2(decay2(both2(dtc), pack2(A[k][2 * q], A[k][2 * q + 1])),

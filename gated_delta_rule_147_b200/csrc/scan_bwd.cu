@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
     if (warp < kWalkers) {
         const int nl = lane % NS, cl = lane / NS, at0 = lane_place<Gm>(warp, 0, cl);
         f2 A[CH][2];
-        load_states<Gm>(A, a.A, tl, a.N, a.state_vec, at0, nl, kLog2e, true);
+        load_states<Gm, true>(A, a.A, tl, a.N, a.state_vec, at0, nl);
         if constexpr (ENDS) {
             f2 h[CH][2], p[CH][2], E[CH][2];
 #pragma unroll

@@ -122,11 +122,11 @@ template <typename Gm> __device__ __forceinline__ int lane_place(int walker, int
     return (walker * Gm::CH + c) * Gm::CL + cl;
 }
 
-// One lane's states of its channels (places p0, p0 + CL, ..), [D, N] (A) or
-// [B, D, N] layout.
-template <typename Gm>
+// One lane's states of its channels (places p0, p0 + CL, ..), [D, N] (A, as decay
+// rates with RATE) or [B, D, N] layout.
+template <typename Gm, bool RATE>
 __device__ __forceinline__ void load_states(f2 (&s)[Gm::CH][2], const float* p, const ScanTile& tl, int N, int vec,
-                                            int p0, int nl, float scale, bool clamp) {
+                                            int p0, int nl) {
 #pragma unroll
     for (int c = 0; c < Gm::CH; ++c) {
         const int ch = place_channel<Gm>(p0 + c * Gm::CL);
@@ -139,13 +139,9 @@ __device__ __forceinline__ void load_states(f2 (&s)[Gm::CH][2], const float* p, 
                 for (int i = 0; i < 4; ++i)
                     if (nl * 4 + i < N) f[i] = q[i];
         }
+        if (RATE)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] *= scale;
-            // A = -inf (a state that holds one token) times dt = 0 of a padded
-            // token would be NaN; the lowest number gives the same decays
-            if (clamp && f[i] < -3.402823466e38f) f[i] = -3.402823466e38f;
-        }
+            for (int i = 0; i < 4; ++i) f[i] = decay_rate(f[i]);
         s[c][0] = pack2(f[0], f[1]);
         s[c][1] = pack2(f[2], f[3]);
     }
@@ -155,7 +151,7 @@ template <typename Gm>
 __device__ __forceinline__ void load_given(f2 (&s)[Gm::CH][2], const float* p, const ScanArgs& a, const ScanTile& tl,
                                            int p0, int nl) {
     if (p) {
-        load_states<Gm>(s, p + (size_t)tl.b * a.D_ * a.N, tl, a.N, a.state_vec, p0, nl, 1.f, false);
+        load_states<Gm, false>(s, p + (size_t)tl.b * a.D_ * a.N, tl, a.N, a.state_vec, p0, nl);
     } else {
 #pragma unroll
         for (int c = 0; c < Gm::CH; ++c) s[c][0] = s[c][1] = both2(0.f);

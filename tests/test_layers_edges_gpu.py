@@ -84,6 +84,25 @@ def test_scan_steps_at_the_upper_end(cuda_device, dtype):
                 assert ok.all()
 
 
+@pytest.mark.parametrize("N", [4, 7, 16, 40])
+def test_scan_nan_decay_shows_in_every_call(cuda_device, N):
+    """A NaN in A reaches the state and the outputs of its channel, and no other, in a
+    prompt and in a single token alike."""
+    B, D = 2, 12
+    r = Rnd(cuda_device, N)
+    i = scan_inputs(r, F32, B, 1, D, N, 1, True, True, True, True, True)
+    i["A"][5, N - 1] = NAN
+    i["A"][7, 0] = NAN
+    bad = torch.zeros(D, dtype=torch.bool, device=cuda_device)
+    bad[[5, 7]] = True
+    kw = dict(delta_bias=i["delta_bias"], delta_softplus=True)
+    y, h = gdr.scan_fwd(*(i[k] for k in ARGS), **kw)
+    h1 = i["h0"].clone()
+    y1 = gdr.scan_step(*(i[k][:, 0] if k in SEQ else i[k] for k in ARGS[:7]), h1, **kw)
+    for y_, h_ in ((y[:, 0], h), (y1, h1)):
+        assert torch.equal(y_.isnan(), bad.expand(B, D)) and torch.equal(h_.isnan(), i["A"].isnan().expand(B, D, N))
+
+
 # ---------------------------------------------------------------- results in place
 
 def test_in_place_refusals(cuda_device):
