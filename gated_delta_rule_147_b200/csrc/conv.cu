@@ -25,9 +25,15 @@ namespace gdr {
 // Backward, 4 x 4096 x 6144: 4 and 4 164 us (4.9 TB/s), 4 and 2 about 190, 2 and 4
 // about 200.
 constexpr int kConvVec = 4, kConvAhead = 4;
+// Backward: a chunk's dweight and dbias are kConvSums sums of 32 tokens or more, 64
+// at most, each left in shared memory when it is complete. One sum over a chunk of
+// 228 tokens (the case above) had twice the error of torch's sums in fp32, 2.9e-7;
+// these have 1.7e-7 (torch's 1.4e-7), in the same time. Chunks of 64 tokens take 195 us.
+constexpr int kConvSums = 4;
 
 struct ConvShape {
     int T, D, nvec, nchunk, tt, silu, w_f32;
+    int sub, subs;   // backward: tokens of a sum, sums of a chunk
     unsigned total;  // threads: B * nchunk * nvec
 };
 
@@ -180,11 +186,16 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const T* __restrict__ x, 
     }
 }
 
+// Blocks per SM of the backward kernel, by the bytes of an element of x and of dy:
+// two where three would spill. Without the bound the compiler places the loads of
+// the case above so that it takes 209 us.
+constexpr int conv_bwd_blocks(int bytes, int W, int how) { return bytes == 8 && W == 4 && how != kWholeRow ? 2 : 3; }
+
 // One chunk of tokens: dx of its rows (and dX0 in the first chunk), and the
 // chunk's partial dw, dbias. dx_s needs dp up to W - 1 tokens on, so the walk
 // runs W - 1 tokens past the chunk; those tokens' dw belongs to the next chunk.
 template <typename T, typename TG, int V, int W, int HOW>
-__global__ void __launch_bounds__(128) conv_bwd_kernel(
+__global__ void __launch_bounds__(128, conv_bwd_blocks(sizeof(T) + sizeof(TG), W, HOW)) conv_bwd_kernel(
     const T* __restrict__ x, const void* __restrict__ weight, const void* __restrict__ bias,
     const T* __restrict__ X0, const int* __restrict__ lengths, const TG* __restrict__ dy,
     const float* __restrict__ dX_T, float* __restrict__ dx, float* __restrict__ dX0, float* __restrict__ part,
@@ -207,11 +218,9 @@ __global__ void __launch_bounds__(128) conv_bwd_kernel(
     load_taps<T, V, W, HOW>(w, bs, weight, bias, c, left, s.w_f32);
     load_window<T, V, W, HOW>(win, xr, X0r, xt, s.D, t0, n, left);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        db[i] = both2(0.f);
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][i] = acc[j][i] = both2(0.f);
-    }
+        for (int j = 0; j < W; ++j) acc[j][i] = both2(0.f);
     // one token: dp from its row and gradient, its share of the sums (SUM), and
     // the gradient of row t - W + 1, complete after it
     auto token = [&](const Row& row, const Grad& grad, bool sum, f2 (&out)[P]) {
@@ -253,106 +262,140 @@ __global__ void __launch_bounds__(128) conv_bwd_kernel(
         }
     }
     float* dxr = dx + ((long long)b * s.T + t0 - (W - 1)) * s.D + c;  // row t - W + 1
-    for (int tb = t0; tb < stop; tb += K) {
-        Row rows[K];
-        Grad grads[K];
-        xp += K * xt;
-        gp += K * gt;
+    static_assert(V == 4, "sums in quads");
+    __shared__ __align__(16) float sums[kConvSums][W + 1][128][V];  // a thread's own
+#pragma unroll 1
+    for (int q = 0, tg = t0; q < s.subs; ++q, tg += s.sub) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            rows[k] = xnext[k];
-            grads[k] = gnext[k];
+        for (int i = 0; i < P; ++i) {
+            db[i] = both2(0.f);
+#pragma unroll
+            for (int j = 0; j < W; ++j) dw[j][i] = both2(0.f);
         }
-        if (tb + 2 * K <= end) {
+        const int te = q + 1 == s.subs ? stop : min(stop, tg + s.sub);
+        for (int tb = tg; tb < te; tb += K) {
+            Row rows[K];
+            Grad grads[K];
+            xp += K * xt;
+            gp += K * gt;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                xnext[k].load(xp + k * xt, left);
-                gnext[k].load(gp + k * gt, left);
+                rows[k] = xnext[k];
+                grads[k] = gnext[k];
             }
-        } else {
+            if (tb + 2 * K <= end) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                xnext[k].zero();
-                gnext[k].zero();
-                if (tb + K + k < end) {
+                for (int k = 0; k < K; ++k) {
                     xnext[k].load(xp + k * xt, left);
                     gnext[k].load(gp + k * gt, left);
                 }
+            } else {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    xnext[k].zero();
+                    gnext[k].zero();
+                    if (tb + K + k < end) {
+                        xnext[k].load(xp + k * xt, left);
+                        gnext[k].load(gp + k * gt, left);
+                    }
+                }
+            }
+            if (tb >= t0 + W - 1 && tb + K <= min(t1, n)) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    f2 out[P];
+                    token(rows[k], grads[k], true, out);
+                    Out::store(dxr, out, left);
+                    dxr += s.D;
+                }
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < K; ++k) {
+                    const int t = tb + k, e = t - (W - 1);
+                    Row row = rows[0];  // rows[k] without an index that is not constant
+                    Grad grad = grads[0];
+#pragma unroll
+                    for (int q = 1; q < K; ++q)
+                        if (q == k) { row = rows[q]; grad = grads[q]; }
+                    f2 out[P];
+                    // a token that is not read has dp = 0: its gradient is 0 and, its
+                    // window being finite, so is dy/dp times it
+                    if (t >= n) {
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            out[i] = acc[0][i];
+#pragma unroll
+                            for (int j = 1; j < W; ++j) acc[j - 1][i] = j < W - 1 ? acc[j][i] : both2(0.f);
+                        }
+                        slide(win);
+                    } else {
+                        token(row, grad, t < t1, out);
+                    }
+                    const bool lead = chunk == 0 && e < 0;  // a carried row
+                    const int tail = e - (n - (W - 1));     // row of X_T that is input row e
+                    if (t < stop && (e >= t0 || lead)) {
+                        if (dX_T && tail >= 0 && tail < W - 1) {
+                            Out d;
+                            d.load(dX_T + ((size_t)b * (W - 1) + tail) * s.D + c, left);
+#pragma unroll
+                            for (int i = 0; i < P; ++i) out[i] = add2(out[i], d.pair(i));
+                        }
+                        if (!lead) Out::store(dxr, out, left);
+                        else if (dX0) Out::store(dX0 + ((size_t)b * (W - 1) + e + W - 1) * s.D + c, out, left);
+                    }
+                    dxr += s.D;
+                }
             }
         }
-        if (tb >= t0 + W - 1 && tb + K <= min(t1, n)) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                f2 out[P];
-                token(rows[k], grads[k], true, out);
-                Out::store(dxr, out, left);
-                dxr += s.D;
-            }
-        } else {
-#pragma unroll 1
-            for (int k = 0; k < K; ++k) {
-                const int t = tb + k, e = t - (W - 1);
-                Row row = rows[0];  // rows[k] without an index that is not constant
-                Grad grad = grads[0];
-#pragma unroll
-                for (int q = 1; q < K; ++q)
-                    if (q == k) { row = rows[q]; grad = grads[q]; }
-                f2 out[P];
-                // a token that is not read has dp = 0: its gradient is 0 and, its
-                // window being finite, so is dy/dp times it
-                if (t >= n) {
-#pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        out[i] = acc[0][i];
-#pragma unroll
-                        for (int j = 1; j < W; ++j) acc[j - 1][i] = j < W - 1 ? acc[j][i] : both2(0.f);
-                    }
-                    slide(win);
-                } else {
-                    token(row, grad, t < t1, out);
-                }
-                const bool lead = chunk == 0 && e < 0;  // a carried row
-                const int tail = e - (n - (W - 1));     // row of X_T that is input row e
-                if (t < stop && (e >= t0 || lead)) {
-                    if (dX_T && tail >= 0 && tail < W - 1) {
-                        Out d;
-                        d.load(dX_T + ((size_t)b * (W - 1) + tail) * s.D + c, left);
-#pragma unroll
-                        for (int i = 0; i < P; ++i) out[i] = add2(out[i], d.pair(i));
-                    }
-                    if (!lead) Out::store(dxr, out, left);
-                    else if (dX0) Out::store(dX0 + ((size_t)b * (W - 1) + e + W - 1) * s.D + c, out, left);
-                }
-                dxr += s.D;
-            }
+        for (int j = 0; j <= W; ++j) {
+            const f2 (&r)[P] = j < W ? dw[j < W ? j : 0] : db;
+            *reinterpret_cast<ulonglong2*>(sums[q][j][threadIdx.x]) = make_ulonglong2(r[0], r[1]);
         }
     }
     float* pr = part + (size_t)r0 * (W + 1) * s.D + c;  // partial sums [b, chunk][W + 1][D]
-#pragma unroll
-    for (int j = 0; j < W; ++j) Out::store(pr + (size_t)j * s.D, dw[j], left);
-    Out::store(pr + (size_t)W * s.D, db, left);
+#pragma unroll 1
+    for (int j = 0; j <= W; ++j) {
+        f2 f[P] = {both2(0.f), both2(0.f)};
+        for (int q = 0; q < s.subs; ++q) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sums[q][j][threadIdx.x]);
+            f[0] = add2(f[0], v.x);
+            f[1] = add2(f[1], v.y);
+        }
+        Out::store(pr + (size_t)j * s.D, f, left);
+    }
 }
 
 // dweight [D, W] and dbias [D] from `parts` partials of [W + 1][D]: 32 columns
-// x 8 slices of the partials per block, slices added in order.
+// x 8 slices of the partials per block, slices added in order. Sums of 16 partials
+// are added in 64 bits: a narrow layer has thousands of partials (8 x 16384 tokens x
+// 64 channels: 8192). All 16 loads are on their way together, those beyond the
+// last partial repeat it.
 __global__ void __launch_bounds__(256) conv_reduce_kernel(const float* __restrict__ part, float* __restrict__ dw,
                                                           float* __restrict__ db, int parts, int D, int W) {
     const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
     const long long cols = (long long)(W + 1) * D;
     const long long col = (long long)blockIdx.x * 32 + lane;
-    __shared__ float sm[8][32];
-    float a = 0.f;
+    __shared__ double sm[8][32];
+    double a = 0.;
     dependent_wait();
     if (col < cols)
-        for (int p = sl; p < parts; p += 8) a += part[(size_t)p * cols + col];
+        for (int p0 = sl; p0 < parts; p0 += 8 * 16) {
+            float v[16], t = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = part[(size_t)min(p0 + 8 * k, parts - 1) * cols + col];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) t += p0 + 8 * k < parts ? v[k] : 0.f;
+            a += t;
+        }
     sm[sl][lane] = a;
     __syncthreads();
     if (sl == 0 && col < cols) {
 #pragma unroll
         for (int k = 1; k < 8; ++k) a += sm[k][lane];
         const int j = (int)(col / D), d = (int)(col - (long long)j * D);
-        if (j < W) dw[(size_t)d * W + j] = a;
-        else if (db) db[d] = a;
+        if (j < W) dw[(size_t)d * W + j] = (float)a;
+        else if (db) db[d] = (float)a;
     }
 }
 
@@ -420,6 +463,11 @@ static int conv_tokens(long long per_token, int T, int lo, int hi, long long wav
 // Resident threads: 7 blocks of 128 (70 registers) and 3 (162) to an SM.
 static int conv_fwd_tokens(int B, int T, int nvec) { return conv_tokens((long long)B * nvec, T, 8, 64, 148 * 7 * 128); }
 static int conv_bwd_tokens(int B, int T, int nvec) { return conv_tokens((long long)B * nvec, T, 16, 256, 148 * 3 * 128); }
+// Tokens of one sum in a chunk of tt, whole batches.
+static int conv_sum_tokens(int tt) {
+    const int sub = (tt + kConvSums - 1) / kConvSums;
+    return sub < 32 ? 32 : (sub + kConvAhead - 1) / kConvAhead * kConvAhead;
+}
 static int conv_vectors(int D) { return (D + kConvVec - 1) / kConvVec; }
 static int conv_chunks(int T, int tt) { return T > 0 ? (T + tt - 1) / tt : 1; }
 
@@ -537,6 +585,8 @@ gdr_status gdr_conv_bwd(const void* x, const void* weight, const void* bias, con
     ConvShape s = {};
     s.T = T; s.D = D; s.nvec = conv_vectors(D);
     s.tt = conv_bwd_tokens(B, T, s.nvec);
+    s.sub = conv_sum_tokens(s.tt);
+    s.subs = (s.tt + s.sub - 1) / s.sub;
     s.nchunk = conv_chunks(T, s.tt);
     s.silu = activation == GDR_ACT_SILU;
     s.w_f32 = weight_dtype == GDR_FP32;

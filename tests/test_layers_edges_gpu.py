@@ -103,6 +103,25 @@ def test_scan_nan_decay_shows_in_every_call(cuda_device, N):
         assert torch.equal(y_.isnan(), bad.expand(B, D)) and torch.equal(h_.isnan(), i["A"].isnan().expand(B, D, N))
 
 
+# ---------------------------------------------------------------- convolution
+
+@pytest.mark.parametrize("B,T,D", [(32, 256, 14208), (8, 32768, 16)])
+def test_conv_parameter_gradients_of_long_sums(cuda_device, B, T, D):
+    """dweight and dbias over many tokens in one thread's chunk, or over many chunks.
+    Every term is 1 + 63 2^-23, which a sum of 128 terms and more loses at every
+    addition: one sum over 256 terms is 60 2^-24 off. Adding n equal numbers to 0 one
+    after the other costs at most (n + 1) / 2 roundings of the sum; sums of 64 terms,
+    of 4 such sums, of 16 partials, and the result's rounding come to 32.5 + 2.5 +
+    8.5 + 1."""
+    v = 1 + 63 * 2.0 ** -23
+    x, dy = (torch.full((1, 1, D), c, device=cuda_device).expand(B, T, D) for c in (1.0, v))
+    w, b = torch.ones(D, 2, device=cuda_device), torch.zeros(D, device=cuda_device)
+    g = gdr.conv_bwd(x, w, b, dy=dy, activation=None)
+    for got, n in ((g["dweight"][:, 1], B * T), (g["dweight"][:, 0], B * (T - 1)), (g["dbias"], B * T)):
+        off = ((got.double() - n * v).abs().max() / (n * v)).item()
+        assert off <= 45 * R.U32, off / R.U32
+
+
 # ---------------------------------------------------------------- results in place
 
 def test_in_place_refusals(cuda_device):
