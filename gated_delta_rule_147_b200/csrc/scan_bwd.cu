@@ -235,9 +235,9 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
         // dy dgate/dz, dt, dyh
         struct Held { Rows u; float sig[Rows::NV][VW], gz[Rows::NV][VW], dt[Rows::NV][VW], dyh[Rows::NV][VW]; } held[2];
         uint32_t* const slots = reinterpret_cast<uint32_t*>(results + 2 * Sh::out);
-        float bias[VW], skip[VW], dD[VW], db[VW];
+        float bias[VW], skip[VW], dD[VW], lost[VW], db[VW];
 #pragma unroll
-        for (int j = 0; j < VW; ++j) dD[j] = db[j] = 0.f;
+        for (int j = 0; j < VW; ++j) dD[j] = lost[j] = db[j] = 0.f;
         channel_values(bias, a.bias, tl, vch);
         channel_values(skip, a.D, tl, vch);
         constexpr int kGrads = 3 * Rows::kWords, kStates = kGrads + Grads::kWords;
@@ -339,7 +339,11 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                     dd[j] = fmaf(uf[j], gB, sd) * h.sig[i][j];
                     dz[j] = z ? h.gz[i][j] * fmaf(skip[j], uf[j], sum_states<Gm>(o + at * NQ)) : 0.f;
                     if (!on) du[j] = dd[j] = dz[j] = 0.f;
-                    dD[j] = on ? fmaf(dyh, uf[j], dD[j]) : dD[j];
+                    // a thread adds hundreds of tokens: what an addition loses goes into the
+                    // next one (without that dD is 3.9e-7 off, with it 0.9e-7)
+                    const float term = on ? fmaf(dyh, uf[j], -lost[j]) : -lost[j], sum = dD[j] + term;
+                    lost[j] = (sum - dD[j]) - term;
+                    dD[j] = sum;
                     db[j] += dd[j];
                 }
                 const size_t row = rbase + (size_t)t * a.D_;
@@ -466,8 +470,10 @@ __global__ void __launch_bounds__(256) scan_reduce_kernel(ScanReduce r) {
     const long long e = (long long)(blockIdx.x - r.bc_blocks) * 256 + threadIdx.x;
     const long long da = (long long)r.D_ * r.N, all = da + 2ll * r.D_;
     if (e >= all) return;
-    float s = 0.f;
-    for (int b = 0; b < r.parts; ++b) s += r.prm[(size_t)b * all + e];
+    double sum = 0.;  // of some 300 chunks at most, or of any number of sequences
+#pragma unroll 8
+    for (int b = 0; b < r.parts; ++b) sum += r.prm[(size_t)b * all + e];
+    const float s = (float)sum;
     if (e < da) r.dA[e] = s;
     else if (e < da + r.D_) { if (r.dD) r.dD[e - da] = s; }
     else if (r.dbias) r.dbias[e - da - r.D_] = s;

@@ -103,6 +103,19 @@ def test_scan_nan_decay_shows_in_every_call(cuda_device, N):
         assert torch.equal(y_.isnan(), bad.expand(B, D)) and torch.equal(h_.isnan(), i["A"].isnan().expand(B, D, N))
 
 
+def test_scan_skip_gradient_of_a_long_sum(cuda_device):
+    """dD of 4096 tokens, 512 a thread. Every term is 1 + 63 2^-23, which a sum of 128
+    terms and more loses at every addition (94 2^-24 in all). With compensated sums
+    2 roundings remain, of 8 threads' sums 4.5, of 2 sequences 1.5."""
+    B, T, D, N = 2, 4096, 9600, 16
+    v = 1 + 63 * 2.0 ** -23
+    u, delta, dy = (torch.full((1, 1, D), c, device=cuda_device).expand(B, T, D) for c in (1.0, 0.1, v))
+    none = torch.zeros(1, 1, 1, N, device=cuda_device).expand(B, T, 1, N)
+    g = gdr.scan_bwd(u, delta, -torch.ones(D, N, device=cuda_device), none, none, torch.ones(D, device=cuda_device), dy=dy)
+    off = ((g["dD"].double() - B * T * v).abs().max() / (B * T * v)).item()
+    assert off <= 8 * R.U32, off / R.U32
+
+
 # ---------------------------------------------------------------- convolution
 
 @pytest.mark.parametrize("B,T,D", [(32, 256, 14208), (8, 32768, 16)])
