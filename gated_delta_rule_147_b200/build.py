@@ -1,5 +1,6 @@
 """Builds the CUDA library in-tree: gated_delta_rule_147_b200/libgdr.so (sm_100a),
-and the Python module of the layer operators beside it, _layers.so.
+and, where torch is installed, the Python module of the layer operators beside
+it, _layers.so.
 
 Each source compiles to its own object (in parallel, under _build/), then one
 link step each makes the shared library and the module (which links to it).
@@ -45,10 +46,18 @@ def _deps():
     return deps
 
 
+def _torch_dir() -> str | None:
+    """Where torch is installed (not imported: only its headers are wanted), or None:
+    the library needs nvcc alone."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MODULE):
+    built = [LIB, MODULE] if _torch_dir() else [LIB]
+    if not all(os.path.exists(f) for f in built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
+    t = min(os.path.getmtime(f) for f in built)
     return any(os.path.getmtime(d) > t for d in _deps())
 
 
@@ -63,7 +72,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     inc = ["-I", os.path.join(ROOT, "include")]
     # a header change rebuilds every object; otherwise only sources newer than their object
     hdr_t = max(os.path.getmtime(d) for d in _deps() if not d.endswith((".cu", ".cpp")))
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)  # not imported: only its headers are wanted
+    torch_dir = _torch_dir()
     cxx = os.environ.get("CXX", "g++")
 
     def compile_one(src: str):
@@ -84,10 +93,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         subprocess.run(cmd, check=True)
 
     with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        for f in [ex.submit(compile_one, s) for s in [BINDING, *SOURCES]]:
+        for f in [ex.submit(compile_one, s) for s in ([BINDING] if torch_dir else []) + SOURCES]:
             f.result()
     link = [_nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", LIB, *[_obj(s) for s in SOURCES]]
     subprocess.run(link, check=True)
+    if not torch_dir:
+        return LIB
     libs = ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     # by name, found beside the module: an absolute path would tie it to this folder
     subprocess.run([cxx, "-shared", "-o", MODULE, _obj(BINDING), "-L", HERE, "-l:libgdr.so", "-L",

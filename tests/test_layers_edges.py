@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from gated_delta_rule_147_b200 import _lib, layers  # noqa: F401
+from gated_delta_rule_147_b200 import _lib, build, layers  # noqa: F401
 from gated_delta_rule_147_b200 import _layers
 
 P = 1 << 20  # a fake, aligned device address that no check follows
@@ -20,3 +20,22 @@ def test_a_result_in_place_has_its_inputs_layout():
         apart("q_out", buf, "q", buf[:, :, :, :1].expand(2, 3, 4, 8), True)
     one = torch.zeros(2, 1, 4, 8)  # an axis of one has no order
     apart("q_out", one.view(2, 4, 1, 8), "q", one.transpose(1, 2), True)
+
+
+def commands_of_a_build(monkeypatch, tmp_path):
+    got = []
+    monkeypatch.setattr(build, "OBJDIR", str(tmp_path / "obj"))
+    monkeypatch.setattr(build.subprocess, "run", lambda cmd, **kw: got.append(list(cmd)))
+    assert build.build(force=True) == build.LIB
+    return got
+
+
+def test_the_library_builds_without_torch(monkeypatch, tmp_path):
+    """C callers need nvcc alone: no torch, then no Python module, but the library."""
+    monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: None)
+    got = commands_of_a_build(monkeypatch, tmp_path)
+    assert not any(build.BINDING in " ".join(c) or build.MODULE in c for c in got)
+    assert sum(c[-1].endswith(".cu") for c in got) == len(build.SOURCES) and build.LIB in got[-1]
+    monkeypatch.setattr(build, "MODULE", str(tmp_path / "none.so"))  # its absence does not call for a build
+    monkeypatch.setattr(build.os.path, "getmtime", lambda f: 1.0)
+    assert not build._stale()
