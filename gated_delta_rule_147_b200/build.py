@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -53,6 +54,14 @@ def _torch_dir() -> str | None:
     return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
+def _cuda_include() -> str:
+    """The headers beside the nvcc in use."""
+    nvcc = _nvcc()
+    if not os.path.isabs(nvcc):
+        nvcc = shutil.which(nvcc) or "/usr/local/cuda/bin/nvcc"
+    return os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
+
+
 def _stale() -> bool:
     built = [LIB, MODULE] if _torch_dir() else [LIB]
     if not all(os.path.exists(f) for f in built):
@@ -83,7 +92,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [_nvcc(), *COMPILE_FLAGS, *inc, "-c", "-o", obj, path]
         if src == BINDING:
             dirs = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include/torch/csrc/api/include"),
-                    sysconfig.get_paths()["include"], "/usr/local/cuda/include"]
+                    sysconfig.get_paths()["include"], _cuda_include()]
             cmd = [cxx, "-O2", "-std=c++17", "-fPIC", *inc, *(f for d in dirs for f in ("-isystem", d)), "-c", "-o", obj,
                    path]
         if verbose:

@@ -39,3 +39,14 @@ def test_the_library_builds_without_torch(monkeypatch, tmp_path):
     monkeypatch.setattr(build, "MODULE", str(tmp_path / "none.so"))  # its absence does not call for a build
     monkeypatch.setattr(build.os.path, "getmtime", lambda f: 1.0)
     assert not build._stale()
+
+
+def test_the_module_builds_with_the_headers_of_the_nvcc_in_use(monkeypatch, tmp_path):
+    nvcc = tmp_path / "cuda" / "bin" / "nvcc"
+    nvcc.parent.mkdir(parents=True)
+    nvcc.write_text("")
+    monkeypatch.setenv("NVCC", str(nvcc))
+    got = commands_of_a_build(monkeypatch, tmp_path)
+    binding = next(c for c in got if c[-1].endswith(build.BINDING))
+    assert str(tmp_path / "cuda" / "include") in binding and "/usr/local/cuda/include" not in binding
+    assert build.MODULE in got[-1]
