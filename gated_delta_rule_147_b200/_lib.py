@@ -90,8 +90,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                          ("gdr_qk_norm_bwd", [vp] * 13 + [sz, vp] + [ip] * 8 + [fp] * 3 + [ip] * 4 + [vp])):
             getattr(lib, fn).argtypes = args
             getattr(lib, fn).restype = ip
-        for fn, n in (("gdr_conv_bwd_workspace_size", 4), ("gdr_scan_bwd_workspace_size", 5),
-                      ("gdr_qk_norm_bwd_workspace_size", 1)):
+        for fn, n in (("gdr_conv_bwd_workspace_size", 4), ("gdr_scan_fwd_workspace_size", 5),
+                      ("gdr_scan_bwd_workspace_size", 5), ("gdr_qk_norm_bwd_workspace_size", 1)):
             getattr(lib, fn).argtypes = [ip] * n
             getattr(lib, fn).restype = sz
         lib.gdr_status_string.argtypes = [ip]

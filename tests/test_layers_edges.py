@@ -50,3 +50,12 @@ def test_the_module_builds_with_the_headers_of_the_nvcc_in_use(monkeypatch, tmp_
     binding = next(c for c in got if c[-1].endswith(build.BINDING))
     assert str(tmp_path / "cuda" / "include") in binding and "/usr/local/cuda/include" not in binding
     assert build.MODULE in got[-1]
+
+
+def test_workspace_sizes_are_declared_as_sizes():
+    """ctypes takes a C int unless told otherwise, which cuts a size to 32 bits."""
+    lib = _lib.load()
+    for name in _lib.EXPORTS:
+        if name.endswith(("_workspace_size", "_capacity")):
+            assert getattr(lib, name).restype is _lib.ctypes.c_size_t, name
+            assert getattr(lib, name).argtypes is not None, name
