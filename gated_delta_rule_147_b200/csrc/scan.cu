@@ -239,10 +239,11 @@ __global__ void __launch_bounds__(kScanThreads, Gm::CH == 2 ? kFwdBlocks : 2 * k
     }
     if (MODE == kScanOut) {
         // rows from the last step on hold no token
-        T* y = reinterpret_cast<T*>(a.y) + (size_t)tl.b * a.T * a.D_ + tl.c0;
-        const int t0 = min(tl.t1, tl.t0 + steps * LT);
-        for (int e = threadIdx.x; e < (tl.t1 - t0) * CB; e += kScanThreads)
-            if (e % CB < tl.kleft) y[(size_t)(t0 + e / CB) * a.D_ + e % CB] = from_f32<T>(0.f);
+        static_assert(kScanThreads % CB == 0, "whole rows of threads");
+        const int ch = threadIdx.x % CB, t0 = min(tl.t1, tl.t0 + steps * LT);
+        T* y = reinterpret_cast<T*>(a.y) + (size_t)tl.b * a.T * a.D_ + tl.c0 + ch;
+        if (ch < tl.kleft)
+            for (int t = t0 + threadIdx.x / CB; t < tl.t1; t += kScanThreads / CB) y[(size_t)t * a.D_] = from_f32<T>(0.f);
     }
 }
 

@@ -116,6 +116,20 @@ def test_scan_skip_gradient_of_a_long_sum(cuda_device):
     assert off <= 8 * R.U32, off / R.U32
 
 
+def test_scan_clears_the_rows_behind_a_short_sequence(cuda_device):
+    """A block clears more than 2^31 places of its channel tile (T times 256)."""
+    T, n = 9_000_000, 5
+    r = Rnd(cuda_device, 51)
+    u, Bm, Cm = r(1, T, 1, dtype=BF), r(1, T, 1, 1, dtype=BF), r(1, T, 1, 1, dtype=BF)
+    A = torch.full((1, 1), -0.5, device=cuda_device)
+    out = torch.full((1, T, 1), NAN, dtype=BF, device=cuda_device)
+    lengths = torch.tensor([n], dtype=torch.int32, device=cuda_device)
+    want, h = gdr.scan_fwd(u[:, :n], u[:, :n].abs(), A, Bm[:, :n], Cm[:, :n])
+    y, h_T = gdr.scan_fwd(u, u.abs(), A, Bm, Cm, lengths=lengths, out=out, workspace=None)
+    assert y is out and torch.equal(y[:, :n], want) and torch.equal(h_T, h)
+    assert (y[:, n:] == 0).all()
+
+
 # ---------------------------------------------------------------- convolution
 
 @pytest.mark.parametrize("B,T,D", [(32, 256, 14208), (8, 32768, 16)])
