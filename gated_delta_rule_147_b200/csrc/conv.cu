@@ -489,7 +489,7 @@ static gdr_status conv_check(const void* weight, const void* bias, int B, int T,
     if (B < 1 || T < 0 || D < 1 || W < 1 || !dtype_ok(dtype) || !dtype_ok(weight_dtype)) return GDR_ERR_INVALID_ARG;
     if (activation != GDR_ACT_NONE && activation != GDR_ACT_SILU) return GDR_ERR_INVALID_ARG;
     if (!weight) return GDR_ERR_INVALID_ARG;
-    if (W < 2 || W > 4) return GDR_ERR_UNSUPPORTED;
+    if (W < 2 || W > 4 || !axes_fit({B, T, D})) return GDR_ERR_UNSUPPORTED;
     if (weight_dtype != dtype && weight_dtype != GDR_FP32) return GDR_ERR_UNSUPPORTED;
     if (!aligned_to(weight, dtype_size(weight_dtype)) || !aligned_to(bias, dtype_size(weight_dtype)))
         return GDR_ERR_MISALIGNED;
@@ -557,7 +557,7 @@ gdr_status gdr_conv_fwd(const void* x, const void* weight, const void* bias, con
 }
 
 size_t gdr_conv_bwd_workspace_size(int B, int T, int D, int W) {
-    if (B < 1 || T < 0 || D < 1 || W < 2 || W > 4) return 0;
+    if (B < 1 || T < 0 || D < 1 || W < 2 || W > 4 || !axes_fit({B, T, D})) return 0;
     const int tt = conv_bwd_tokens(B, T, conv_vectors(D));
     return round256((size_t)B * conv_chunks(T, tt) * (W + 1) * D * sizeof(float));
 }

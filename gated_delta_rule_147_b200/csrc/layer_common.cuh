@@ -3,6 +3,8 @@
 // activations, packed fp32 pairs, and the launch as a programmatic dependent.
 #pragma once
 
+#include <initializer_list>
+
 #include "common.cuh"
 
 namespace gdr {
@@ -334,6 +336,14 @@ cudaError_t launch_dependent(void (*kern)(KArgs...), unsigned grid, unsigned blo
 }
 
 // Host checks shared by the entry points.
+// Tokens, channels and sequences are counted in int, and some loops and roundings
+// count a little past the last one (a chunk, a step on its way).
+constexpr int kMaxAxis = 0x7fffffff - 4096;
+inline bool axes_fit(std::initializer_list<long long> axes) {
+    for (long long n : axes)
+        if (n > kMaxAxis) return false;
+    return true;
+}
 inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline size_t dtype_size(int dtype) { return dtype == GDR_BF16 ? 2 : 4; }
 inline bool dtype_ok(int dtype) { return dtype == GDR_BF16 || dtype == GDR_FP32; }

@@ -548,7 +548,7 @@ static gdr_status norm_fill(NormArgs& a, const long long* strides, int nstrides,
     if (pos64 != 0 && pos64 != 1) return GDR_ERR_INVALID_ARG;
     if ((Hk > 0) != (k != nullptr) && T > 0) return GDR_ERR_INVALID_ARG;
     if ((Hk == 0 && kw) || (T > 0 && !q)) return GDR_ERR_INVALID_ARG;
-    if (d > 256) return GDR_ERR_UNSUPPORTED;
+    if (d > 256 || !axes_fit({(long long)Hq + Hk})) return GDR_ERR_UNSUPPORTED;
     if (weight_dtype != dtype && weight_dtype != GDR_FP32) return GDR_ERR_UNSUPPORTED;
     const size_t e = dtype_size(dtype), ew = dtype_size(weight_dtype);
     if (!aligned_to(q, e) || !aligned_to(k, e) || !aligned_to(qw, ew) || !aligned_to(kw, ew) ||

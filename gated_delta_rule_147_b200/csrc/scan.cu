@@ -285,7 +285,7 @@ int scan_chunks(int B, int T, int K, int N, int G) {
 void scan_split(ScanArgs& a, int chunks, int CH) {
     const int per = (a.T + chunks - 1) / chunks;
     a.chunk = per < 32 ? 32 : (per + 31) / 32 * 32;
-    a.chunks = a.T > 0 ? (a.T + a.chunk - 1) / a.chunk : 1;
+    a.chunks = a.T > 0 ? (a.T - 1) / a.chunk + 1 : 1;
     a.tiles = scan_tiles(a.K, a.N, CH);
 }
 size_t scan_ends_bytes(int B, int G, int K, int N, int chunks, int CH) {

@@ -25,7 +25,7 @@ static gdr_status scan_fill(ScanArgs& a, const void* u, const void* delta, const
                             int G, int delta_softplus, int dtype) {
     if (B < 1 || T < 0 || D_ < 1 || N < 1 || G < 1 || D_ % G || !dtype_ok(dtype)) return GDR_ERR_INVALID_ARG;
     if (!A || (T > 0 && (!u || !delta || !Bm || !Cm))) return GDR_ERR_INVALID_ARG;
-    if (N > 128) return GDR_ERR_UNSUPPORTED;
+    if (N > 128 || !axes_fit({B, T, D_})) return GDR_ERR_UNSUPPORTED;
     const size_t e = dtype_size(dtype);
     for (const void* p : {u, delta, Bm, Cm, z})
         if (!aligned_to(p, e)) return GDR_ERR_MISALIGNED;
@@ -73,7 +73,7 @@ static gdr_status launched(cudaError_t e) { return e == cudaSuccess ? GDR_OK : G
 extern "C" {
 
 size_t gdr_scan_fwd_workspace_size(int B, int T, int D_, int N, int G) {
-    if (B < 1 || T < 0 || D_ < 1 || N < 1 || N > 128 || G < 1 || D_ % G) return 0;
+    if (B < 1 || T < 0 || D_ < 1 || N < 1 || N > 128 || G < 1 || D_ % G || !axes_fit({B, T, D_})) return 0;
     return scan_ends_bytes(B, G, D_ / G, N, scan_chunks(B, T, D_ / G, N, G), 2);
 }
 
@@ -99,7 +99,7 @@ gdr_status gdr_scan_fwd(const void* u, const void* delta, const float* A, const 
 }
 
 size_t gdr_scan_bwd_workspace_size(int B, int T, int D_, int N, int G) {
-    if (B < 1 || T < 0 || D_ < 1 || N < 1 || N > 128 || G < 1 || D_ % G) return 0;
+    if (B < 1 || T < 0 || D_ < 1 || N < 1 || N > 128 || G < 1 || D_ % G || !axes_fit({B, T, D_})) return 0;
     return scan_bwd_layout(B, T, D_, N, G, scan_bwd_chunks(B, T, D_ / G, N, G)).total;
 }
 

@@ -104,7 +104,7 @@ struct ScanTile {
         c0 = g * a.K + tile * cb;
         kleft = min(cb, a.K - tile * cb);
         t0 = part * a.chunk;
-        t1 = min(a.T, t0 + a.chunk);
+        t1 = a.T - t0 < a.chunk ? a.T : t0 + a.chunk;
         n = max(t0, min(t1, seq_len(a.lengths, b, a.T)));
     }
 };

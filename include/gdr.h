@@ -396,6 +396,8 @@ gdr_status gdr_decode_step_grouped(const void* q, const void* k, const void* v,
  *   or GDR_FP32 (so fp32 gradients of gdr_chunk_bwd can be handed on); gradients
  *   of inputs are fp32, written completely and deterministic (no atomics).
  *   Sums, states and norms are fp32; an output is rounded once.
+ * Sizes: sequences, tokens, channels and heads (H_q + H_k) are at most
+ *   2^31 - 4097 each (GDR_ERR_UNSUPPORTED above).
  * Errors as for the recurrence, on the host and before any launch; a pointer
  *   that is not element-aligned gives GDR_ERR_MISALIGNED. None of these kernels
  *   waits on anything that another launch writes, so there is no status word.

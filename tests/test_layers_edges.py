@@ -59,3 +59,48 @@ def test_workspace_sizes_are_declared_as_sizes():
         if name.endswith(("_workspace_size", "_capacity")):
             assert getattr(lib, name).restype is _lib.ctypes.c_size_t, name
             assert getattr(lib, name).argtypes is not None, name
+
+
+LONGEST = 2 ** 31 - 1 - 4096
+
+
+def entry(fn, **kw):
+    """Status of one entry point, with fake pointers and dense arrays."""
+    a = dict(B=1, T=1, D=1, W=2, N=1, G=1, H=1, Hk=1, d=1)
+    a.update(kw)
+    lib, n = _lib.load(), None
+    B, T, D, W, N, G, H, Hk, d = (a[k] for k in ("B", "T", "D", "W", "N", "G", "H", "Hk", "d"))
+    if fn == "conv_fwd":
+        return lib.gdr_conv_fwd(P, P, n, n, n, P, n, n, B, T, D, W, 0, 0, 0, n)
+    if fn == "conv_bwd":
+        return lib.gdr_conv_bwd(P, P, n, n, n, P, n, P, P, n, n, P, 1 << 50, n, B, T, D, W, 0, 0, 0, 0, n)
+    if fn == "conv_step":
+        return lib.gdr_conv_step(P, P, n, P, P, n, B, D, W, 0, 0, 0, n)
+    if fn == "scan_fwd":
+        return lib.gdr_scan_fwd(P, P, P, P, P, n, n, n, n, n, P, n, n, 0, n, B, T, D, N, G, 0, 0, n)
+    if fn == "scan_bwd":
+        return lib.gdr_scan_bwd(P, P, P, P, P, n, n, n, n, n, P, n, P, P, P, P, P, n, n, n, n, P, 1 << 50, n, B, T, D, N, G,
+                                0, 0, 0, n)
+    if fn == "scan_step":
+        return lib.gdr_scan_step(P, P, P, P, P, n, n, n, P, P, n, B, D, N, G, 0, 0, n)
+    if fn == "qk_norm_fwd":
+        return lib.gdr_qk_norm_fwd(P, P, n, n, n, n, P, P, n, B, T, H, Hk, d, 0, 0, 0, 1e-6, 1.0, 1.0, 0, 0, 0, n)
+    return lib.gdr_qk_norm_bwd(P, P, n, n, n, n, P, P, P, P, n, n, n, 0, n, B, T, H, Hk, d, 0, 0, 0, 1e-6, 1.0, 1.0, 0, 0, 0,
+                               0, n)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake pointers: for hosts without a GPU")
+@pytest.mark.parametrize("fn,axes", [("conv_fwd", "BTD"), ("conv_bwd", "BTD"), ("conv_step", "BD"), ("scan_fwd", "BTD"),
+                                     ("scan_bwd", "BTD"), ("scan_step", "BD"), ("qk_norm_fwd", "H"), ("qk_norm_bwd", "H")])
+def test_axes_that_the_kernels_would_count_past_are_refused(fn, axes):
+    """Chunks, steps and vectors are rounded up and counted in int."""
+    for ax in axes:
+        for size in (2 ** 31 - 1, LONGEST + 1):
+            assert entry(fn, **{ax: size}) == _lib.GDR_ERR_UNSUPPORTED, (ax, size)
+    if fn.startswith("qk_norm"):
+        assert entry(fn, H=2 ** 30, Hk=2 ** 30) == _lib.GDR_ERR_UNSUPPORTED
+    sizes = {"conv_bwd": lambda T: _lib.gdr_conv_bwd_workspace_size(1, T, 1, 2),
+             "scan_fwd": lambda T: _lib.gdr_scan_fwd_workspace_size(1, T, 1, 1, 1),
+             "scan_bwd": lambda T: _lib.gdr_scan_bwd_workspace_size(1, T, 1, 1, 1)}
+    if fn in sizes:
+        assert sizes[fn](LONGEST + 1) == 0 and sizes[fn](LONGEST) > 0
