@@ -53,7 +53,7 @@ __device__ __forceinline__ void load_taps(f2 (&w)[W][V / 2], f2 (&bias)[V / 2], 
     } else {
 #pragma unroll
         for (int i = 0; i < V * W; ++i)
-            flat[i] = i >= left * W ? 0.f
+            flat[i] = i / W >= left ? 0.f
                       : w_f32 ? reinterpret_cast<const float*>(weight)[(size_t)c * W + i]
                               : to_f32(reinterpret_cast<const T*>(weight)[(size_t)c * W + i]);
     }

@@ -149,6 +149,21 @@ def test_conv_parameter_gradients_of_long_sums(cuda_device, B, T, D):
         assert off <= 45 * R.U32, off / R.U32
 
 
+@pytest.mark.parametrize("W,D", [(4, (1 << 29) + 2), (2, (1 << 30) + 1)])
+def test_conv_of_a_very_wide_layer(cuda_device, W, D):
+    """More than 2^31 filter taps: the first and last channels as in a layer of their own."""
+    x = torch.randn(1, 1, D, device=cuda_device, dtype=BF)
+    w = torch.randn(D, W, device=cuda_device, dtype=BF)
+    y, X = gdr.conv_fwd(x, w)
+    for s in (slice(0, 6), slice(D // 2, D // 2 + 6), slice(D - 5, D)):
+        want, X_want = gdr.conv_fwd(x[..., s], w[s].clone())
+        assert torch.equal(y[..., s], want) and torch.equal(X[..., s], X_want)
+    del y, X
+    one = torch.zeros(1, W - 1, D, device=cuda_device, dtype=BF)
+    y = gdr.conv_step(x[:, 0], w, None, one)
+    assert torch.equal(y[:, :6], gdr.conv_fwd(x[..., :6], w[:6].clone())[0][:, 0])
+
+
 # ---------------------------------------------------------------- results in place
 
 def test_in_place_refusals(cuda_device):
