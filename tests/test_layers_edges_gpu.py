@@ -193,3 +193,25 @@ def test_in_place_refusals(cuda_device):
     want, _ = gdr.qk_norm_fwd(buf)
     got, _ = gdr.qk_norm_fwd(buf, q_out=buf)
     assert got is buf and torch.equal(buf, want)
+
+
+# ---------------------------------------------------------------- norm and rotation
+
+@pytest.mark.parametrize("dtype,d,rot", [(BF, 256, 64), (F32, 72, 72), (BF, 114, 56)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_norm_backward_of_more_tokens_than_one_turn(cuda_device, dtype, d, rot, layout):
+    """More blocks of tokens than are launched: positions, turns and the weights' sums
+    go on from one turn to the next (5103 tokens, 319 blocks of 16 or more of fewer;
+    296 are launched), the last one partly filled."""
+    B, T, Hq, Hk = 3, 1701, 2, 1
+    r = Rnd(cuda_device, d)
+    q, k, dq, dk = (r(B, T, H, d, dtype=dtype) for H in (Hq, Hk, Hq, Hk))
+    qw, kw = r(d), r(d)
+    f = torch.exp(-torch.arange(rot // 2) / 3.0).to(cuda_device)
+    p = r.ints(-(1 << 20), 1 << 20, B, T)
+    kws = dict(kind="rms", eps=1e-5, q_scale=0.5, positions=p, inv_freq=f, rotary=layout)
+    g = gdr.qk_norm_bwd(q, k, qw, kw, dq=dq, dk=dk, **kws)
+    for x, w, do, n, s, H in ((q, qw, dq, "q", 0.5, Hq), (k, kw, dk, "k", 1.0, Hk)):
+        v, m = R.norm(x, w, "rms", 1e-5, s, p, f, layout, 1.0, do)
+        R.check(g["d" + n], v["dx"], m["dx"], 100, "d" + n)
+        R.check(g[f"d{n}_weight"], v["dw"], m["dw"], 100 + B * T * H, f"d{n}_weight")
