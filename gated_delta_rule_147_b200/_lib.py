@@ -16,9 +16,6 @@ GDR_OK, GDR_ERR_INVALID_ARG, GDR_ERR_UNSUPPORTED, GDR_ERR_MISALIGNED, GDR_ERR_LA
 GDR_DEVICE_TIMEOUT, GDR_DEVICE_DECAY_RANGE = 1, 2
 GDR_BF16, GDR_FP32 = 0, 1
 GATE_NONE, GATE_SCALAR, GATE_CHANNEL, GATE_TIED = 0, 1, 2, 3
-ACT_NONE, ACT_SILU = 0, 1
-NORM_L2, NORM_RMS = 0, 1
-ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
 
 EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_grouped", "gdr_chunk_fwd_workspace_size",
            "gdr_chunk_fwd_static", "gdr_chunk_fwd_static_capacity", "gdr_chunk_bwd",
