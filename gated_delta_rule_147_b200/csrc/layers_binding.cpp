@@ -16,6 +16,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <climits>
 #include <cstring>
 #include <string>
@@ -75,6 +76,11 @@ const Tensor& required(PyObject* o, const char* name) {
 }
 int code_of(at::ScalarType t) { return t == at::kBFloat16 ? GDR_BF16 : GDR_FP32; }
 
+// An axis's size as the library's int.
+int64_t counted(const char* name, int64_t n) {
+    if (n > INT_MAX) bad_value(std::string(name) + " has an axis of " + std::to_string(n) + "; the library counts in int");
+    return n;
+}
 // Type code of the tensor that the others are held to.
 int first(const char* name, const Tensor& t, int ndim) {
     if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat)
@@ -82,8 +88,7 @@ int first(const char* name, const Tensor& t, int ndim) {
     if (!t.is_cuda()) bad_value(std::string(name) + " is on " + t.device().str() + "; the library takes CUDA tensors");
     if (t.dim() != ndim)
         bad_value(std::string(name) + " has " + std::to_string(t.dim()) + " axes; expected " + std::to_string(ndim));
-    for (int64_t n : t.sizes())
-        if (n > INT_MAX) bad_value(std::string(name) + " has an axis of " + std::to_string(n) + "; the library counts in int");
+    for (int64_t n : t.sizes()) counted(name, n);
     return code_of(t.scalar_type());
 }
 void axes(const char* name, const Tensor& t, int ndim) {
@@ -275,7 +280,7 @@ struct ConvArgs {
         const auto dev = x.device();
         D = x.size(ndim - 1);
         axes("weight", weight, 2);
-        W = (int)weight.size(1);
+        W = (int)counted("weight", weight.size(1));
         dense("weight", &weight, {D, W}, param, dev);
         dense("bias", bias, {D}, weight.scalar_type(), dev);
         act = choice(activation, "activation", {{"silu", GDR_ACT_SILU}, {"none", GDR_ACT_NONE}}, "'silu' or None",
@@ -380,8 +385,8 @@ struct ScanTensors {
         B = u.size(0);
         T = n == 2 ? u.size(1) : 1;
         Dn = u.size(n);
-        N = A.size(1);
-        G = Bm.size(n);
+        N = counted("A", A.size(1));
+        G = counted("Bm", Bm.size(n));
         dense("A", &A, {Dn, N}, at::kFloat, dev);
         dense("D", D, {Dn}, at::kFloat, dev);
         dense("delta_bias", bias, {Dn}, at::kFloat, dev);
@@ -502,7 +507,7 @@ struct NormTensors {
         for (int i = 0; i < 3; ++i) st[i] = q.stride(i);
         if (k) {
             axes("k", *k, 4);
-            Hk = k->size(2);
+            Hk = counted("k", k->size(2));
             check("k", *k, {B, T, Hk, d}, own, dev);
             for (int i = 0; i < 3; ++i) st[3 + i] = k->stride(i);
         }
@@ -517,8 +522,8 @@ struct NormTensors {
         rotary = choice(a[9], "rotary", {{"half", GDR_ROTARY_HALF}, {"interleaved", GDR_ROTARY_INTERLEAVED}},
                         "'half' or 'interleaved'");
         if (freq) {
-            rot = (int)(2 * freq->numel());
-            dense("inv_freq", freq, {rot / 2}, at::kFloat, dev);
+            rot = (int)std::min<int64_t>(2 * freq->numel(), INT_MAX - 1);  // even; refused where above d
+            dense("inv_freq", freq, {freq->numel()}, at::kFloat, dev);
         }
         if (pos) {
             check("positions", *pos, {B, T}, Types(at::kInt, at::kLong), dev, 0);

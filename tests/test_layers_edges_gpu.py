@@ -164,6 +164,20 @@ def test_conv_of_a_very_wide_layer(cuda_device, W, D):
     assert torch.equal(y[:, :6], gdr.conv_fwd(x[..., :6], w[:6].clone())[0][:, 0])
 
 
+def test_axes_beyond_int_are_refused(cuda_device):
+    """Heads, groups and states too: cut to 32 bits they would be 1 or 4."""
+    n = (1 << 32) + 1
+    q = torch.zeros(1, 1, 1, 1, device=cuda_device, dtype=BF)
+    with pytest.raises(ValueError, match="k has an axis of 4294967297"):
+        gdr.qk_norm_fwd(q, q.expand(1, 1, n, 1))
+    u, A = torch.zeros(1, 1, 1, device=cuda_device, dtype=BF), torch.zeros(1, 1, device=cuda_device)
+    with pytest.raises(ValueError, match="Bm has an axis of 4294967297"):
+        wide = torch.empty(1, 1, n, 1, device=cuda_device, dtype=BF)
+        gdr.scan_fwd(u, u, A, wide, wide)
+    with pytest.raises(ValueError, match="A has an axis of 4294967297"):
+        gdr.scan_fwd(u, u, torch.empty(1, n, device=cuda_device), wide.view(1, 1, 1, n), wide.view(1, 1, 1, n))
+
+
 # ---------------------------------------------------------------- results in place
 
 def test_in_place_refusals(cuda_device):
