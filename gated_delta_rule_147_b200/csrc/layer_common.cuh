@@ -130,7 +130,8 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 }
 
 // 1 / (1 + e^-x) from the hardware exponential and reciprocal; e^-x = inf
-// gives 0. Relative error a few 2^-23 (the exponent's argument is rounded once).
+// gives 0. Relative error a few 2^-24, and for negative x about 1.3 |x| 2^-24 more:
+// the product x log2(e) and log2(e) itself are rounded.
 __device__ __forceinline__ float sigmoidf_fast(float x) {
     return rcp_approx(1.f + ex2_approx(-x * kLog2e));
 }

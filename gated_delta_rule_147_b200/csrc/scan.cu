@@ -274,7 +274,10 @@ template <typename F> static cudaError_t dispatch_scan_lanes(int ns, F&& f) {
 }
 
 // Chunks of the tokens: as many as fill two blocks per SM, of 256 tokens at
-// least, and none below three (see above).
+// least, and none below three (see above). One sequence of 2048 channels x 16
+// states in bf16: 768 tokens 37.5 us split and 58.7 whole, 4096 106 and 298. The
+// 256 is not borne out for short sequences: with 64, 512 tokens would take 20.6 us
+// where they now take 40.5, and 768 27.3; from 2048 on nothing changes.
 int scan_chunks(int B, int T, int K, int N, int G) {
     const long long units = (long long)B * G * scan_tiles(K, N, 2);
     const long long c = units > 0 ? 148 * kFwdBlocks / units : 0, most = T / 256;

@@ -483,8 +483,10 @@ cudaError_t launch_scan_ckpt(const ScanArgs& a, int B, int dtype, cudaStream_t s
 void scan_split(ScanArgs& a, int chunks, int CH);
 size_t scan_ends_bytes(int B, int G, int K, int N, int chunks, int CH);
 
-// Chunks of the backward pass: the maps cost a
-// third walk beside two, so two chunks pay already.
+// Chunks of the backward pass: the maps cost a third walk beside two, so two chunks
+// pay already. One sequence of 2048 channels x 16 states in bf16: 384 tokens 79.5 us
+// whole, 512 78.3 in two chunks. The 256 tokens at least are not borne out for short
+// sequences: with 64, 384 would take 52.4 us and 512 63.2; from 1024 on nothing changes.
 int scan_bwd_chunks(int B, int T, int K, int N, int G) {
     const long long units = (long long)B * G * scan_tiles(K, N, 1);
     const long long c = units > 0 ? 148 * kBwdBlocks / units : 0, most = T / 256;

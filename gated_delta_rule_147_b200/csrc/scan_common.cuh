@@ -18,7 +18,7 @@
 // conversions and global accesses fill the issue slots between its exponentials.
 // (All of it in one warp, with segments of 8 tokens per warp and their states
 // joined by a barrier per 64 tokens, ran at 0.47 instructions per cycle: 856 us
-// for 4 x 4096 tokens x 4096 channels x 16 states, against 485 us.)
+// for 4 x 4096 tokens x 4096 channels x 16 states, against 490 us.)
 #pragma once
 
 #include "layer_common.cuh"
@@ -72,7 +72,7 @@ template <int NS_, int CH_, int VW_, int STEPS_> struct ScanGeom {
     // the helpers move rows in vectors of VW channels
     static constexpr int VW = VW_ < CB ? VW_ : CB, VPT = CB / VW;
 };
-// Forward, 4 x 4096 tokens x 4096 channels x 16 states (485 us): 2 channels a lane
+// Forward, 4 x 4096 tokens x 4096 channels x 16 states (490 us): 2 channels a lane
 // and 2 blocks per SM; 1 channel and 4 blocks took 1.21 times as long, 1 and 3
 // 1.29 times. Backward, its checkpoints too, 2 x 4096 x 4096 x 16, ragged (1030
 // us): 1 channel and 2 blocks; 2 and 1 took 1.17 times as long. The vectors give

@@ -395,7 +395,7 @@ gdr_status gdr_decode_step_grouped(const void* q, const void* k, const void* v,
  *   and delta_bias are fp32. Gradients of outputs have `grad_dtype`, `dtype`
  *   or GDR_FP32 (so fp32 gradients of gdr_chunk_bwd can be handed on); gradients
  *   of inputs are fp32, written completely and deterministic (no atomics).
- *   Sums, states and norms are fp32; an output is rounded once.
+ *   Sums, states and norms are fp32 or more; an output is rounded once.
  * Sizes: sequences, tokens, channels and heads (H_q + H_k) are at most
  *   2^31 - 4097 each (GDR_ERR_UNSUPPORTED above).
  * Errors as for the recurrence, on the host and before any launch; a pointer
@@ -486,8 +486,9 @@ size_t gdr_scan_fwd_workspace_size(int B, int T, int D_, int N, int G);
  * and ddelta_bias are NULL exactly when z, D and delta_bias are; dh0 may be
  * NULL and needs h0. strides: as gdr_scan_fwd, then dy batch, token.
  * workspace: at least gdr_scan_bwd_workspace_size() bytes, 256-byte aligned
- * (the state every 8 tokens, sums of dB and dC per 64 channels of 16 states, sums
- * of the parameter gradients per sequence).
+ * (the state every 8 tokens, every 4 where N <= 8; sums of dB and dC per block of
+ * channels, 32 of them with 16 states, more with fewer; sums of the parameter
+ * gradients per sequence and chunk of tokens).
  */
 gdr_status gdr_scan_bwd(const void* u, const void* delta, const float* A, const void* Bm,
                         const void* Cm, const float* D, const void* z, const float* delta_bias,
@@ -527,7 +528,7 @@ gdr_status gdr_scan_step(const void* u, const void* delta, const float* A, const
  * dense (likewise k). 1 <= d <= 256, rot even and at most d, eps > 0. Angles
  * are reduced exactly, with inv_freq / (2 pi) held to 53 bits: an error of
  * position * inv_freq * 2^-53 radians. A row's sum of squares must stay within
- * fp32. Loads and stores are wide where d is a multiple of 8, strides likewise
+ * fp32; in a row (or a row's gradient) that is not finite other elements may be NaN too. Loads and stores are wide where d is a multiple of 8, strides likewise
  * and arrays are 16-byte aligned.
  */
 gdr_status gdr_qk_norm_fwd(const void* q, const void* k, const void* q_weight,
