@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(kScanThreads, kBwdBlocks) scan_bwd_kernel(Scan
                     // a thread adds hundreds of tokens: what an addition loses goes into the
                     // next one (without that dD is 3.9e-7 off, with it 0.9e-7)
                     const float term = on ? fmaf(dyh, uf[j], -lost[j]) : -lost[j], sum = dD[j] + term;
-                    lost[j] = (sum - dD[j]) - term;
+                    // finite (NaN gives the bound), so that an infinite sum stays infinite
+                    lost[j] = fminf(fmaxf((sum - dD[j]) - term, -1e36f), 1e36f);
                     dD[j] = sum;
                     db[j] += dd[j];
                 }

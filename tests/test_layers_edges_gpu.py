@@ -116,6 +116,22 @@ def test_scan_skip_gradient_of_a_long_sum(cuda_device):
     assert off <= 8 * R.U32, off / R.U32
 
 
+def test_scan_skip_gradient_that_overflows(cuda_device):
+    """An infinite sum stays infinite, and with its channel."""
+    T, D, N = 40, 8, 4
+    r = Rnd(cuda_device, 61)
+    u, Bm, Cm = r(1, T, D), r(1, T, 1, N), torch.zeros(1, T, 1, N, device=cuda_device)
+    dy = torch.ones_like(u)
+    u[0, 3::2, 2], dy[0, 3::2, 2] = 1e30, 1e30
+    u[0, :, 5], dy[0, :, 5] = -3e38, 1.0
+    g = gdr.scan_bwd(u, torch.full_like(u, 0.1), -torch.ones(D, N, device=cuda_device), Bm, Cm, torch.ones(D, device=cuda_device),
+                     dy=dy)
+    want = (u * dy).sum((0, 1))
+    assert want[2] == INF and want[5] == -INF
+    assert torch.equal(g["dD"].isinf(), want.isinf()) and g["dD"][2] == INF and g["dD"][5] == -INF
+    assert torch.isfinite(g["dD"][[0, 1, 3, 4, 6, 7]]).all()
+
+
 def test_scan_clears_the_rows_behind_a_short_sequence(cuda_device):
     """A block clears more than 2^31 places of its channel tile (T times 256)."""
     T, n = 9_000_000, 5
