@@ -528,8 +528,9 @@ gdr_status gdr_scan_step(const void* u, const void* delta, const float* A, const
  * dense (likewise k). 1 <= d <= 256, rot even and at most d, eps > 0. Angles
  * are reduced exactly, with inv_freq / (2 pi) held to 53 bits: an error of
  * position * inv_freq * 2^-53 radians. A row's sum of squares must stay within
- * fp32; in a row (or a row's gradient) that is not finite other elements may be NaN too. Loads and stores are wide where d is a multiple of 8, strides likewise
- * and arrays are 16-byte aligned.
+ * fp32; where an element of a row is not finite, others of it may be NaN too.
+ * Loads and stores are wide where d is a multiple of 8, strides likewise and
+ * arrays are 16-byte aligned.
  */
 gdr_status gdr_qk_norm_fwd(const void* q, const void* k, const void* q_weight,
                            const void* k_weight, const void* positions, const float* inv_freq,
